@@ -34,3 +34,16 @@ from ._lib import (  # noqa: F401
     sl_validate_payload,
     sl_validate_payloads,
 )
+from ._ops import (  # noqa: F401
+    SL_MAX_ALTERNATIVES,
+    SL_NEWTON_SCHULZ,
+    muon_step,
+    muon_step_workspace,
+    orthogonalize,
+    orthogonalize_workspace,
+    sl_muon_step,
+    sl_orthogonalize,
+    sl_token_logprobs,
+    token_logprobs,
+    token_logprobs_workspace,
+)

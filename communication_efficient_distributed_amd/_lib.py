@@ -31,7 +31,9 @@ STATUS = {
 EXPORTS = ("sl_compress", "sl_compress_weights", "sl_aggregate", "sl_aggregate_interleaved", "sl_aggregate_apply",
            "sl_aggregate_apply_interleaved",
            "sl_apply_mean", "sl_validate_payload", "sl_validate_payloads", "sl_peer_stats",
-           "sl_peer_stats_interleaved", "sl_peer_stats_noalloc", "sl_host_device_pointer", "sl_status_string")
+           "sl_peer_stats_interleaved", "sl_peer_stats_noalloc", "sl_host_device_pointer", "sl_status_string",
+           "sl_orthogonalize", "sl_orthogonalize_workspace", "sl_muon_step", "sl_muon_step_workspace",
+           "sl_token_logprobs", "sl_token_logprobs_workspace")
 
 
 class SparseLoCoError(RuntimeError):
@@ -86,6 +88,19 @@ def load():
     L.sl_apply_mean.restype = ctypes.c_int
     L.sl_status_string.argtypes = [ctypes.c_int]
     L.sl_status_string.restype = ctypes.c_char_p
+    L.sl_orthogonalize_workspace.argtypes = [I64, I64, I64, I32]
+    L.sl_orthogonalize_workspace.restype = I64
+    L.sl_orthogonalize.argtypes = [P, I32, I64, I64, P, I32, I64, I64, I64, I64, I64, P, I32, F32, I32, P, I64, P]
+    L.sl_orthogonalize.restype = ctypes.c_int
+    L.sl_muon_step_workspace.argtypes = [I64, I64, I64, I32]
+    L.sl_muon_step_workspace.restype = I64
+    L.sl_muon_step.argtypes = [P, I32, P, P, I32, I64, I64, I64, F32, F32, I32, F32, F32, F32, P, I32, F32, I32, P, I64,
+                               P]
+    L.sl_muon_step.restype = ctypes.c_int
+    L.sl_token_logprobs_workspace.argtypes = [I64, I64, I32, I32]
+    L.sl_token_logprobs_workspace.restype = I64
+    L.sl_token_logprobs.argtypes = [P, I32, I64, P, I64, I64, I32, P, P, P, P, P, I64, P]
+    L.sl_token_logprobs.restype = ctypes.c_int
     _handle = L
     return L
 

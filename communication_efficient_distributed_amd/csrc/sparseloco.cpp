@@ -375,9 +375,9 @@ sl_status sl_host_device_pointer(const void* host_ptr, void** device_ptr) {
 const char* sl_status_string(int status) {
     switch (status) {
         case SL_OK: return "SL_OK";
-        case SL_ERR_INVALID_ARG: return "SL_ERR_INVALID_ARG: null pointer, non-finite beta or overlapping buffers";
-        case SL_ERR_SHAPE: return "SL_ERR_SHAPE: n must be a non-negative multiple of 4096";
-        case SL_ERR_ALIGN: return "SL_ERR_ALIGN: dense and payload buffers need 16-byte alignment, scales 4-byte";
+        case SL_ERR_INVALID_ARG: return "SL_ERR_INVALID_ARG: null pointer, non-finite or refused value, overlapping buffers or short workspace";
+        case SL_ERR_SHAPE: return "SL_ERR_SHAPE: a size is outside its documented range (n must be a non-negative multiple of 4096)";
+        case SL_ERR_ALIGN: return "SL_ERR_ALIGN: a buffer is not aligned as documented (dense and payload buffers 16 bytes, scales 4)";
         case SL_ERR_TOO_MANY_PEERS: return "SL_ERR_TOO_MANY_PEERS: n_peers outside the allowed range";
         case SL_ERR_HIP: return "SL_ERR_HIP: the HIP runtime reported a launch error";
         default: return "unknown sl_status";
