@@ -11,7 +11,7 @@ import ctypes
 
 import torch
 
-from ._lib import _check, _dev, _stream_of, load
+from ._lib import _check, load
 
 SL_MAX_ALTERNATIVES = 32
 SL_PRODUCTS_F16 = 0
@@ -22,22 +22,47 @@ _PRODUCTS = {"f16": SL_PRODUCTS_F16, "split": SL_PRODUCTS_SPLIT}
 # (a, b, c) of each step X <- a X + (b A + c A A) X, A = X X^T: singular values
 # of 0.003 and more reach [0.68, 1.21] in five steps.
 SL_NEWTON_SCHULZ = ((3.4445, -4.7750, 2.0315),) * 5
+_STANDARD = (ctypes.c_float * 15)(*[v for step in SL_NEWTON_SCHULZ for v in step])
 
 
 def _gpu(t: torch.Tensor, name: str, dtypes) -> torch.Tensor:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor (got {t.device})")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {', '.join(str(d) for d in dtypes)} (got {t.dtype})")
     return t
 
 
-def _same_device(first: torch.Tensor, **others) -> None:
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} must be on {first.device} (got {t.device})")
+def _buffer(t: torch.Tensor | None, name: str, dtype, shape, device) -> int | None:
+    """Address of a contiguous GPU tensor of this type, shape and device (None stays None)."""
+    if t is None:
+        return None
+    _gpu(t, name, (dtype,))
+    if t.shape != shape:
+        raise ValueError(f"{name} must be of shape {list(shape)} (got {list(t.shape)})")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device} (got {t.device})")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _call(name: str, device, args, stream) -> None:
+    """Calls the library with the device current and the stream last; torch's
+    device guard only where another device is current, since it costs as much
+    as a kernel launch."""
+    handle = torch.cuda.current_stream(device).cuda_stream if stream is None else \
+        int(stream.cuda_stream if hasattr(stream, "cuda_stream") else stream)
+    fn = getattr(load(), name)
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, handle)
+    if status:
+        _check(name, status)
 
 
 def _strided(t: torch.Tensor, name: str):
@@ -56,6 +81,8 @@ def _strided(t: torch.Tensor, name: str):
 
 
 def _coefficients(steps):
+    if steps is SL_NEWTON_SCHULZ:
+        return _STANDARD, len(steps)
     flat = [float(v) for step in steps for v in step]
     if len(flat) != 3 * len(steps):
         raise ValueError("coefficients must be (a, b, c) for each step")
@@ -71,20 +98,25 @@ def _products(products, dtype) -> int:
 
 
 def _workspace(fn: str, need: int, workspace, device, stream):
-    """The caller's workspace, checked, or one from torch's allocator."""
+    """(workspace, address, bytes): the caller's, checked, or one from torch's
+    allocator; the first is held until the call is made."""
     if need < 0:
         raise ValueError(f"{fn}: sizes outside the documented range")
     if workspace is None:
+        if need == 0:
+            return None, None, 0
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
         if stream is not None:
             # torch may hand the memory out again on its own stream: tell it who uses it
-            workspace.record_stream(stream if hasattr(stream, "cuda_stream")
-                                    else torch.cuda.ExternalStream(int(stream), device=device))
-    elif workspace.numel() * workspace.element_size() < need:
-        raise ValueError(f"{fn}: workspace of {workspace.numel() * workspace.element_size()} bytes, {need} needed")
+            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(
+                int(stream.cuda_stream if hasattr(stream, "cuda_stream") else stream), device=device))
+        return workspace, workspace.data_ptr(), need
+    have = workspace.numel() * workspace.element_size()
+    if have < need:
+        raise ValueError(f"{fn}: workspace of {have} bytes, {need} needed")
     if not workspace.is_contiguous() or workspace.device != device:
         raise ValueError(f"{fn}: workspace must be contiguous and on {device}")
-    return workspace, ctypes.c_void_p(workspace.data_ptr()), workspace.numel() * workspace.element_size()
+    return workspace, workspace.data_ptr(), have
 
 
 def orthogonalize_workspace(rows: int, cols: int, count: int = 1, products: str = "f16") -> int:
@@ -112,7 +144,8 @@ def sl_orthogonalize(x: torch.Tensor, out: torch.Tensor, coefficients=SL_NEWTON_
     of orthogonalize_workspace() bytes to use again; by default one from torch's
     allocator."""
     _gpu(x, "x", _TYPES), _gpu(out, "out", _TYPES)
-    _same_device(x, out=out)
+    if out.device != x.device:
+        raise ValueError(f"out must be on {x.device} (got {out.device})")
     if x.shape != out.shape:
         raise ValueError("x and out shapes differ")
     rows, cols, count, x_ld, x_stride = _strided(x, "x")
@@ -121,10 +154,9 @@ def sl_orthogonalize(x: torch.Tensor, out: torch.Tensor, coefficients=SL_NEWTON_
     steps, n_steps = _coefficients(coefficients)
     need = load().sl_orthogonalize_workspace(rows, cols, count, mode)
     keep, ws, ws_bytes = _workspace("sl_orthogonalize", need, workspace, x.device, stream)
-    with torch.cuda.device(x.device):
-        _check("sl_orthogonalize", load().sl_orthogonalize(
-            x.data_ptr(), _TYPES[x.dtype], x_ld, x_stride, out.data_ptr(), _TYPES[out.dtype], out_ld, out_stride,
-            rows, cols, count, steps, n_steps, eps, mode, ws, ws_bytes, _stream_of(x, stream)))
+    _call("sl_orthogonalize", x.device,
+          (x.data_ptr(), _TYPES[x.dtype], x_ld, x_stride, out.data_ptr(), _TYPES[out.dtype], out_ld, out_stride,
+           rows, cols, count, steps, n_steps, eps, mode, ws, ws_bytes), stream)
 
 
 def sl_muon_step(theta: torch.Tensor, momentum: torch.Tensor, grad: torch.Tensor, lr: float, grad_scale: float = 1.0,
@@ -139,24 +171,21 @@ def sl_muon_step(theta: torch.Tensor, momentum: torch.Tensor, grad: torch.Tensor
     grad_scale 1 / n_peers.  products and workspace as for sl_orthogonalize
     (default by theta's type)."""
     _gpu(theta, "theta", (torch.float32, torch.bfloat16)), _gpu(grad, "grad", (torch.float32, torch.bfloat16))
-    _gpu(momentum, "momentum", (torch.float32,))
     if theta.dim() not in (2, 3):
         raise ValueError("theta must be [rows, cols] or [count, rows, cols]")
-    if momentum.shape != theta.shape or grad.shape != theta.shape:
-        raise ValueError("theta, momentum and grad shapes differ")
-    _same_device(theta, momentum=momentum, grad=grad)
-    rows, cols = theta.shape[-2:]
-    count = theta.shape[0] if theta.dim() == 3 else 1
+    dev, shape = theta.device, theta.shape
+    buffers = (_buffer(theta, "theta", theta.dtype, shape, dev), _TYPES[theta.dtype],
+               _buffer(momentum, "momentum", torch.float32, shape, dev),
+               _buffer(grad, "grad", grad.dtype, shape, dev), _TYPES[grad.dtype])
+    rows, cols = shape[-2:]
+    count = shape[0] if len(shape) == 3 else 1
     mode = _products(products, theta.dtype)
     steps, n_steps = _coefficients(coefficients)
-    args = (_dev(theta, "theta", theta.dtype), _TYPES[theta.dtype], _dev(momentum, "momentum", torch.float32),
-            _dev(grad, "grad", grad.dtype), _TYPES[grad.dtype])
     need = load().sl_muon_step_workspace(rows, cols, count, mode)
-    keep, ws, ws_bytes = _workspace("sl_muon_step", need, workspace, theta.device, stream)
-    with torch.cuda.device(theta.device):
-        _check("sl_muon_step", load().sl_muon_step(
-            *args, rows, cols, count, grad_scale, decay, int(bool(nesterov)), lr, weight_decay, update_scale,
-            steps, n_steps, eps, mode, ws, ws_bytes, _stream_of(theta, stream)))
+    keep, ws, ws_bytes = _workspace("sl_muon_step", need, workspace, dev, stream)
+    _call("sl_muon_step", dev,
+          (*buffers, rows, cols, count, grad_scale, decay, int(bool(nesterov)), lr, weight_decay, update_scale,
+           steps, n_steps, eps, mode, ws, ws_bytes), stream)
 
 
 def sl_token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None, logprob: torch.Tensor | None,
@@ -172,30 +201,23 @@ def sl_token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None, logpro
     if logits.dim() != 2:
         raise ValueError("logits must be [rows, vocab]")
     rows, vocab, _, ld, _ = _strided(logits, "logits")
+    if vocab == 0:
+        raise ValueError("logits must have a vocabulary")
     if (top_logprob is None) != (top_index is None):
         raise ValueError("top_logprob and top_index come together")
     if logprob is not None and targets is None:
         raise ValueError("logprob needs targets")
     n_top = 0 if top_index is None else top_index.shape[-1]
-    for name, t, shape, dtype in (("targets", targets, (rows,), torch.int64), ("logprob", logprob, (rows,), torch.float32),
-                                  ("entropy", entropy, (rows,), torch.float32),
-                                  ("top_logprob", top_logprob, (rows, n_top), torch.float32),
-                                  ("top_index", top_index, (rows, n_top), torch.int32)):
-        if t is not None:
-            _dev(t, name, dtype)
-            if tuple(t.shape) != shape:
-                raise ValueError(f"{name} must be of shape {list(shape)}")
-    _same_device(logits, targets=targets, logprob=logprob, entropy=entropy, top_logprob=top_logprob, top_index=top_index)
-    if vocab == 0:
-        raise ValueError("logits must have a vocabulary")
-    need = load().sl_token_logprobs_workspace(rows, vocab, _TYPES[logits.dtype], n_top)
-    keep, ws, ws_bytes = _workspace("sl_token_logprobs", need, workspace, logits.device, stream)
-    ptr = [ctypes.c_void_p(t.data_ptr() if t is not None else None)
-           for t in (targets, logprob, entropy, top_logprob, top_index)]
-    with torch.cuda.device(logits.device):
-        _check("sl_token_logprobs", load().sl_token_logprobs(
-            logits.data_ptr(), _TYPES[logits.dtype], ld, ptr[0], rows, vocab, n_top, *ptr[1:], ws, ws_bytes,
-            _stream_of(logits, stream)))
+    dev, kind = logits.device, _TYPES[logits.dtype]
+    buffers = (_buffer(logprob, "logprob", torch.float32, (rows,), dev),
+               _buffer(entropy, "entropy", torch.float32, (rows,), dev),
+               _buffer(top_logprob, "top_logprob", torch.float32, (rows, n_top), dev),
+               _buffer(top_index, "top_index", torch.int32, (rows, n_top), dev))
+    target = _buffer(targets, "targets", torch.int64, (rows,), dev)
+    need = load().sl_token_logprobs_workspace(rows, vocab, kind, n_top)
+    keep, ws, ws_bytes = _workspace("sl_token_logprobs", need, workspace, dev, stream)
+    _call("sl_token_logprobs", dev,
+          (logits.data_ptr(), kind, ld, target, rows, vocab, n_top, *buffers, ws, ws_bytes), stream)
 
 
 # Convenience wrappers that allocate outputs with torch (device memory only).
@@ -222,7 +244,7 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, n_top: int = 0, 
     top_index), the last two None for n_top = 0."""
     _gpu(logits, "logits", _TYPES)
     rows, dev = logits.shape[0], logits.device
-    logprob, entropy = (torch.empty(rows, dtype=torch.float32, device=dev) for _ in range(2))
+    logprob, entropy = torch.empty((2, rows), dtype=torch.float32, device=dev).unbind(0)
     top_logprob = torch.empty((rows, n_top), dtype=torch.float32, device=dev) if n_top else None
     top_index = torch.empty((rows, n_top), dtype=torch.int32, device=dev) if n_top else None
     sl_token_logprobs(logits, targets, logprob, entropy, top_logprob, top_index, workspace, stream)

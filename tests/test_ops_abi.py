@@ -87,13 +87,13 @@ def test_muon_step_argument_checks(lib):
         assert muon(lib, **kw) == SL_ERR_ALIGN, kw
 
 
-def score(lib, x=X, t=0, ld=1000, targets=T, rows=8, vocab=1000, n_top=4, lp=LP, en=EN, tl=TL, ti=TI, ws=WS, wsb=A):
+def score(lib, x=X, t=0, ld=30000, targets=T, rows=8, vocab=30000, n_top=4, lp=LP, en=EN, tl=TL, ti=TI, ws=WS, wsb=A):
     return lib.sl_token_logprobs(x, t, ld, targets, rows, vocab, n_top, lp, en, tl, ti, ws, wsb, None)
 
 
 def test_token_logprobs_argument_checks(lib):
     assert score(lib, rows=0) == SL_OK
-    for kw in (dict(rows=-1), dict(rows=1 << 31), dict(vocab=0), dict(vocab=(1 << 22) + 1), dict(ld=999),
+    for kw in (dict(rows=-1), dict(rows=1 << 31), dict(vocab=0), dict(vocab=(1 << 22) + 1), dict(ld=29999),
                dict(ld=1 << 60)):
         assert score(lib, **kw) == SL_ERR_SHAPE, kw
     for kw in (dict(t=3), dict(n_top=-1), dict(n_top=33), dict(x=None), dict(targets=None), dict(tl=None), dict(ti=None),
