@@ -35,7 +35,7 @@ typedef _Float16 half4 __attribute__((ext_vector_type(4)));
 typedef float float16v __attribute__((ext_vector_type(16)));
 
 constexpr float kScaleX = 8192.0f, kScaleA = 4096.0f, kScaleB = 2048.0f;
-constexpr int kSumBlocks = 512;  // partial sums of squares per matrix, at most
+constexpr int kSumBlocks = 1024;  // partial sums of squares per matrix, at most
 
 // ---------------------------------------------------------------------------
 // The start: sums of squares (with the momentum update), then X and X^T.
@@ -64,26 +64,51 @@ __device__ __forceinline__ double block_sum(double v, double* lds) {
 
 // partial[i * gridDim.x + block] = the block's share of matrix i's sum of u^2
 // in fp64 (no overflow or underflow for any finite fp32 values); momentum is
-// updated on the way.  Blocks take pieces of 2048 columns of a row in turn.
+// updated on the way.  Blocks take pieces of 2048 columns of a row in turn, a
+// thread eight columns of each: in one go where the rows' alignment allows it
+// (VECTOR), else 256 apart.
+template <bool VECTOR>
 __global__ __launch_bounds__(256) void sum_squares_kernel(Source s, int64_t rows, int64_t cols, double* partial) {
     __shared__ double lds[4];
     const int64_t i = blockIdx.y;
-    const int64_t pieces = (cols + 2047) / 2048;
+    const int pieces = (int)((cols + 2047) / 2048);
     double acc = 0;
     for (int64_t t = blockIdx.x; t < rows * pieces; t += gridDim.x) {
-        const int64_t r = t / pieces, c0 = (t % pieces) * 2048;
+        const int64_t r = t / pieces;
+        const int64_t c0 = (t - r * pieces) * 2048 + (VECTOR ? threadIdx.x * 8 : threadIdx.x);
         const int64_t at = i * s.stride + r * s.ld;
         float* m = s.momentum ? s.momentum + (i * rows + r) * cols : nullptr;
-        for (int64_t c = c0 + threadIdx.x; c < cols && c < c0 + 2048; c += 256) {
-            float u = load_value(s.x, s.type, at + c);
-            if (m) {
-                const float g = u * s.grad_scale;
-                u = momentum_next(g, m[c], s.decay);
-                m[c] = u;
-                if (s.nesterov) u = __builtin_fmaf(s.decay, u, g);
+        float u[8], old[8];
+        if (VECTOR) {
+            if (c0 >= cols) continue;
+            load_values8(s.x, s.type, at + c0, u);
+            if (m) load_values8(m, SL_F32, c0, old);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const bool in = c0 + e * 256 < cols;
+                u[e] = in ? load_value(s.x, s.type, at + c0 + e * 256) : 0.0f;
+                old[e] = in && m ? m[c0 + e * 256] : 0.0f;
             }
-            acc = fma((double)u, (double)u, acc);
         }
+        if (m) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float g = u[e] * s.grad_scale;
+                old[e] = momentum_next(g, old[e], s.decay);
+                u[e] = s.nesterov ? __builtin_fmaf(s.decay, old[e], g) : old[e];
+            }
+            if (VECTOR) {
+                *reinterpret_cast<float4*>(m + c0) = make_float4(old[0], old[1], old[2], old[3]);
+                *reinterpret_cast<float4*>(m + c0 + 4) = make_float4(old[4], old[5], old[6], old[7]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (c0 + e * 256 < cols) m[c0 + e * 256] = old[e];
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc = fma((double)u[e], (double)u[e], acc);
     }
     acc = block_sum(acc, lds);
     if (threadIdx.x == 0) partial[i * gridDim.x + blockIdx.x] = acc;
@@ -105,24 +130,30 @@ __global__ __launch_bounds__(256) void start_kernel(Source s, int64_t rows, int6
     __shared__ double sums[4];
     __shared__ float tile[64][65];
     const int64_t i = blockIdx.z;
+    const int64_t r0 = (int64_t)blockIdx.y * 64, c0 = (int64_t)blockIdx.x * 64;
+    const int tc = threadIdx.x & 63, tr = threadIdx.x >> 6;
+    // The tile's values are on their way while the norm is summed.
+    float u[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        const int64_t r = r0 + tr + 4 * k;
+        const bool in = r < rows && c0 + tc < cols;
+        u[k] = in && !(s.momentum && !s.nesterov) ? load_value(s.x, s.type, i * s.stride + r * s.ld + c0 + tc) : 0.0f;
+        if (s.momentum && in) {
+            const float m = s.momentum[(i * rows + r) * cols + c0 + tc];
+            u[k] = s.nesterov ? __builtin_fmaf(s.decay, m, u[k] * s.grad_scale) : m;
+        }
+    }
     double acc = 0;
     for (int k = threadIdx.x; k < n_partial; k += 256) acc += partial[i * n_partial + k];
     const double norm = sqrt(block_sum(acc, sums)) + (double)eps;
     const double scale = norm > 0 ? (double)kScaleX / norm : 0;
     direct = reinterpret_cast<_Float16*>(reinterpret_cast<char*>(direct) + i * matrix_bytes);
     turned = reinterpret_cast<_Float16*>(reinterpret_cast<char*>(turned) + i * matrix_bytes);
-    const int64_t r0 = (int64_t)blockIdx.y * 64, c0 = (int64_t)blockIdx.x * 64;
-    const int tc = threadIdx.x & 63, tr = threadIdx.x >> 6;
-    for (int r = tr; r < 64; r += 4) {
-        float v = 0;
-        if (r0 + r < rows && c0 + tc < cols) {
-            float u = load_value(s.x, s.type, i * s.stride + (r0 + r) * s.ld + c0 + tc);
-            if (s.momentum) {
-                const float m = s.momentum[(i * rows + r0 + r) * cols + c0 + tc];
-                u = s.nesterov ? __builtin_fmaf(s.decay, m, u * s.grad_scale) : m;
-            }
-            v = (float)((double)u * scale);
-        }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        const int r = tr + 4 * k;
+        const float v = (float)((double)u[k] * scale);
         tile[r][tc] = v;
         _Float16 h, l;
         split_half(v, &h, &l);
@@ -144,6 +175,7 @@ __global__ __launch_bounds__(256) void start_kernel(Source s, int64_t rows, int6
 // The products.
 
 enum { kGram, kPoly, kStep, kLast };
+constexpr bool symmetric(int kind) { return kind == kGram || kind == kPoly; }
 
 struct ProductArgs {
     const _Float16 *p, *q;  // operands: rows of ldp / ldq elements along the summed index
@@ -152,6 +184,8 @@ struct ProductArgs {
     int64_t matrix_bytes;    // from one matrix's arrays to the next one's
     int32_t k_steps;         // summed index / 64
     int32_t tiles_i, tiles_j;
+    int32_t slices;          // of the summed index; with more than one, sums go to `part`
+    float4* part;
     // epilogue
     const _Float16* old;     // poly: A; step, last: X, so that old[j * ldold + i] meets C[i][j]
     int64_t ldold;
@@ -163,15 +197,19 @@ struct ProductArgs {
     // last
     MatrixView out;
     int64_t out_i, out_j;    // extent of out along i (its columns) and j (its rows)
+    bool out_aligned;        // four elements of out along i can be moved at once
     bool diag_by_i;
     bool update;             // theta <- theta * keep - move * O
     float keep, move;
 };
 
 // Copies 16 bytes per lane from global memory to LDS, lane l's to lds + 16 l.
+// In assembler because the compiler makes later LDS reads wait for such copies
+// where it cannot tell the stages apart; arrive() waits for those that matter.  No register is
+// written, and m0 (the LDS address) needs one wait state before its use.
 __device__ __forceinline__ void load_to_lds(const _Float16* src, _Float16* lds) {
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)src,
-                                     (__attribute__((address_space(3))) uint32_t*)lds, 16, 0, 0);
+    const uint32_t to = uniform((uint32_t)(uintptr_t)(__attribute__((address_space(3))) _Float16*)lds);
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(to) : "memory", "m0");
 }
 
 // Tile (ti, tj) of block t.  Symmetric products: the tiles with tj <= ti, in
@@ -215,149 +253,40 @@ __device__ __forceinline__ int xcd_order(int b, int n) {
     return x * q + min(x, r) + (b >> 3);
 }
 
-struct Yes {
-    static constexpr bool value = true;
-};
-struct No {
-    static constexpr bool value = false;
-};
+constexpr int strip_pitch(int ti) { return 32 * ti + 4; }
 
-// Orders the instructions of one quarter: a fragment read (and LOADS / 2 T
-// loads to LDS) ahead of every T / 2 products, so that neither queue empties.
-template <int T, int LOADS>
-__device__ __forceinline__ void interleave() {
-#pragma unroll
-    for (int k = 0; k < 2 * T; ++k) {
-        if constexpr (LOADS > 0) __builtin_amdgcn_sched_group_barrier(0x10, LOADS / (2 * T), 0);
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x8, T * T >= 2 * T ? T / 2 : 1, 0);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-}
-
-// C = P Q^T over tiles of 64 T x 64 T, four wavefronts of 32 T x 32 T each.
-template <int T, bool SPLIT, int KIND>
-__global__ __launch_bounds__(256, 1) void product_kernel(ProductArgs g) {
-    constexpr int B = 64 * T;
-    __shared__ __attribute__((aligned(128))) _Float16 lds[2][2][B * 64];
-    const int lane = lane_id(), wave = uniform(threadIdx.x >> 6);
-    const int wi = wave >> 1, wj = wave & 1;
-    const int tiles = (KIND == kGram || KIND == kPoly) ? g.tiles_i * (g.tiles_i + 1) / 2 : g.tiles_i * g.tiles_j;
-    const int t = xcd_order(blockIdx.x, gridDim.x);
-    const int64_t matrix = t / tiles;
-    int ti, tj;
-    if (KIND == kGram || KIND == kPoly)
-        symmetric_tile(t % tiles, g.tiles_i, &ti, &tj);
-    else
-        full_tile(t % tiles, g.tiles_i, g.tiles_j, &ti, &tj);
+// Finishes 32 columns of C for one wavefront: sums[a], as the matrix
+// instructions leave them (lane l, register r: C[i][j] with
+// i = 32 a + 8 (r / 4) + 4 (l / 32) + r % 4 and j = l % 32), rows from i0,
+// columns from j0.  They pass through the wavefront's strip of LDS: rows of
+// consecutive i from there meet the old values, the transpose ct and the
+// output along memory; then (the finished values put back) columns give the
+// rows of c.
+template <int TI, bool SPLIT, int KIND>
+__device__ __forceinline__ void finish_strip(const ProductArgs& g, int64_t matrix, int64_t i0, int64_t j0, bool on_diagonal,
+                                             const float16v (&sums)[TI], float* strip) {
+    constexpr int W = 32 * TI, kPitch = strip_pitch(TI);
+    constexpr int kTogether = 4 * TI < 8 ? 4 * TI : 8;  // loads in flight, within the register file
+    const int lane = lane_id();
     const int64_t shift = matrix * (g.matrix_bytes / 2);
-
-    // Loads: a wavefront instruction fills 8 rows of 64 elements.  The 16-byte
-    // piece c of row r sits at position c ^ (r & 7), so that the reads below,
-    // same piece of 8 rows, meet 8 different positions.
-    const int lr = lane >> 3, lc = (lane & 7) ^ lr;
-    const _Float16* p = g.p + shift + ((int64_t)ti * B + wave * 8 + lr) * g.ldp + lc * 8;
-    const _Float16* q = g.q + shift + ((int64_t)tj * B + wave * 8 + lr) * g.ldq + lc * 8;
-    const int steps = SPLIT ? 3 * g.k_steps : g.k_steps;
-    auto issue = [&](int s, int buf) {
-        int64_t kp, kq;
-        if (SPLIT) {
-            const int k = s / 3, part = s - 3 * k;  // hi hi, hi lo, lo hi of the same 64 columns in turn
-            kp = (int64_t)k * 64 + (part == 2 ? g.lo : 0);
-            kq = (int64_t)k * 64 + (part == 1 ? g.lo : 0);
-        } else {
-            kp = kq = (int64_t)s * 64;
-        }
-#pragma unroll
-        for (int a = 0; a < 2 * T; ++a) {
-            load_to_lds(p + kp + a * 32 * g.ldp, &lds[buf][0][(a * 32 + wave * 8) * 64]);
-            load_to_lds(q + kq + a * 32 * g.ldq, &lds[buf][1][(a * 32 + wave * 8) * 64]);
-        }
-    };
-    half8 fp[2][T], fq[2][T];
-    const int row_p = wi * 32 * T + (lane & 31), row_q = wj * 32 * T + (lane & 31);
-    auto fetch = [&](int buf, int sub, int into) {
-        const int pos = ((sub * 2 + (lane >> 5)) ^ (lane & 7)) * 8;
-#pragma unroll
-        for (int a = 0; a < T; ++a) {
-            fp[into][a] = *reinterpret_cast<const half8*>(&lds[buf][0][(row_p + a * 32) * 64 + pos]);
-            fq[into][a] = *reinterpret_cast<const half8*>(&lds[buf][1][(row_q + a * 32) * 64 + pos]);
-        }
-    };
-    float16v acc[T][T];
-#pragma unroll
-    for (int a = 0; a < T; ++a)
-#pragma unroll
-        for (int b = 0; b < T; ++b) acc[a][b] = 0.0f;
-    auto multiply = [&](int from) {
-#pragma unroll
-        for (int a = 0; a < T; ++a)
-#pragma unroll
-            for (int b = 0; b < T; ++b)
-                acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fp[from][a], fq[from][b], acc[a][b], 0, 0, 0);
-    };
-
-    // One step: the fragments of each quarter of the 64 columns are fetched while
-    // the matrix cores work on the quarter before.
-    auto step = [&](int s, auto more, auto again) {
-        const int buf = s & 1;
-#pragma unroll
-        for (int sub = 0; sub < 3; ++sub) {
-            fetch(buf, sub + 1, (sub + 1) & 1);
-            multiply(sub & 1);
-            interleave<T, 0>();
-        }
-        // Every wavefront has its last fragments of this buffer and its own
-        // loads of the next one have landed: after the barrier that holds for
-        // all of them.
-        __syncthreads();
-        if constexpr (again.value) issue(s + 2, buf);
-        if constexpr (more.value) fetch(buf ^ 1, 0, 0);
-        multiply(1);
-        if constexpr (again.value) interleave<T, 4 * T>();
-    };
-    issue(0, 0);
-    __syncthreads();
-    if (steps > 1) issue(1, 1);
-    fetch(0, 0, 0);
-    int s = 0;
-    for (; s + 2 < steps; ++s) step(s, Yes{}, Yes{});
-    if (s + 1 < steps) step(s++, Yes{}, No{});
-    step(s, No{}, No{});
-
-    // Lane l holds, for register r of block (a, b), C[i][j] with
-    // i = 8 (r / 4) + 4 (l / 32) + r % 4 and j = l % 32 within the block.
-    // Every wavefront passes its sums, 32 columns j at a time, through its own
-    // quarter of the LDS: rows of consecutive i from there meet the old values,
-    // the transpose ct and the output along memory, then (the finished values
-    // put back) columns give the rows of c.
-    constexpr int W = 32 * T, kPitch = W + 4;
-    float* strip = reinterpret_cast<float*>(&lds[0][0][0]) + wave * (B * 64 / 2);
-    static_assert(32 * kPitch <= B * 64 / 2, "a strip fits a quarter of the LDS");
-    const int64_t i0 = (int64_t)ti * B + wi * W, j0 = (int64_t)tj * B + wj * W;
-    const bool on_diagonal = (KIND == kGram || KIND == kPoly) && ti == tj;
     const float* diag_in = KIND == kGram ? nullptr : g.diag_in + matrix * (g.matrix_bytes / 4);
-    float* diag_out = g.diag_out + matrix * (g.matrix_bytes / 4);
+    float* diag_out = symmetric(KIND) ? g.diag_out + matrix * (g.matrix_bytes / 4) : nullptr;
 #pragma unroll
-    for (int b = 0; b < T; ++b) {
-        const int jb = b * 32;
+    for (int a = 0; a < TI; ++a)
 #pragma unroll
-        for (int a = 0; a < T; ++a)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                float4 v = {acc[a][b][r * 4], acc[a][b][r * 4 + 1], acc[a][b][r * 4 + 2], acc[a][b][r * 4 + 3]};
-                *reinterpret_cast<float4*>(&strip[(lane & 31) * kPitch + a * 32 + r * 8 + 4 * (lane >> 5)]) = v;
-            }
-        wave_sync();
-        constexpr int kTogether = 4 * T < 8 ? 4 * T : 8;  // loads in flight, within the register file
+        for (int r = 0; r < 4; ++r) {
+            const float4 v = {sums[a][r * 4], sums[a][r * 4 + 1], sums[a][r * 4 + 2], sums[a][r * 4 + 3]};
+            *reinterpret_cast<float4*>(&strip[(lane & 31) * kPitch + a * 32 + r * 8 + 4 * (lane >> 5)]) = v;
+        }
+    wave_sync();
 #pragma unroll 1
-        for (int it0 = 0; it0 < 4 * T; it0 += kTogether) {
+    for (int it0 = 0; it0 < 4 * TI; it0 += kTogether) {
         half4 oh[kTogether], ol[kTogether];
         if (KIND != kGram) {
 #pragma unroll
             for (int it = 0; it < kTogether; ++it) {
                 const int at = (it0 + it) * 64 + lane;
-                const _Float16* old = g.old + shift + (j0 + jb + at / (8 * T)) * g.ldold + i0 + at % (8 * T) * 4;
+                const _Float16* old = g.old + shift + (j0 + at / (8 * TI)) * g.ldold + i0 + at % (8 * TI) * 4;
                 oh[it] = *reinterpret_cast<const half4*>(old);
                 if (SPLIT) ol[it] = *reinterpret_cast<const half4*>(old + g.lo);
             }
@@ -365,8 +294,8 @@ __global__ __launch_bounds__(256, 1) void product_kernel(ProductArgs g) {
 #pragma unroll
         for (int it = 0; it < kTogether; ++it) {
             const int at = (it0 + it) * 64 + lane;
-            const int jj = at / (8 * T), ii = at % (8 * T) * 4;
-            const int64_t i = i0 + ii, j = j0 + jb + jj;
+            const int jj = at / (8 * TI), ii = at % (8 * TI) * 4;
+            const int64_t i = i0 + ii, j = j0 + jj;
             float4* cell = reinterpret_cast<float4*>(&strip[jj * kPitch + ii]);
             const float4 sum = *cell;
             float v[4] = {sum.x, sum.y, sum.z, sum.w}, w[4];
@@ -408,7 +337,23 @@ __global__ __launch_bounds__(256, 1) void product_kernel(ProductArgs g) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] = (g.k.a + dd[e]) * w[e] + v[e] * (1.0f / kScaleB);  // times kScaleX
             }
-            if (KIND != kLast) {
+            if (KIND == kLast) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] *= 1.0f / kScaleX;
+                if (g.out_aligned && i + 4 <= g.out_i) {
+                    if (j < g.out_j) {
+                        const int64_t to = matrix * g.out.stride + j * g.out.ld + i;
+                        if (g.update) {
+                            float o[4];
+                            load_values4(g.out.ptr, g.out.type, to, o);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(-g.move, v[e], o[e] * g.keep);
+                        }
+                        store_values4(g.out.ptr, g.out.type, to, v);
+                    }
+                    continue;
+                }
+            } else {
                 half4 h, l;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -423,41 +368,222 @@ __global__ __launch_bounds__(256, 1) void product_kernel(ProductArgs g) {
             }
             *cell = make_float4(v[0], v[1], v[2], v[3]);
         }
-        }
-        wave_sync();
-        if (KIND == kLast) {
-            // 64 consecutive i of one j at a time, whatever the output's type and alignment.
+    }
+    wave_sync();
+    if (KIND == kLast) {
+        // What four at once did not reach: consecutive i, one element per lane.
+        const int64_t done = g.out_aligned ? g.out_i & ~(int64_t)3 : 0;
+        if (i0 + W > done)
 #pragma unroll 4
-            for (int it = 0; it < 16 * T; ++it) {
+            for (int it = 0; it < 16 * TI; ++it) {
                 const int at = it * 64 + lane;
-                const int64_t i = i0 + at % W, j = j0 + jb + at / W;
-                if (i < g.out_i && j < g.out_j) {
+                const int64_t i = i0 + at % W, j = j0 + at / W;
+                if (i >= done && i < g.out_i && j < g.out_j) {
                     const int64_t to = matrix * g.out.stride + j * g.out.ld + i;
-                    float o = strip[(at / W) * kPitch + at % W] * (1.0f / kScaleX);
+                    float o = strip[(at / W) * kPitch + at % W];
                     if (g.update) o = __builtin_fmaf(-g.move, o, load_value(g.out.ptr, g.out.type, to) * g.keep);
                     store_value(g.out.ptr, g.out.type, to, o);
                 }
             }
-        } else if (!on_diagonal) {
+    } else if (!on_diagonal) {
 #pragma unroll 4
-            for (int it = 0; it < 4 * T; ++it) {
-                const int at = it * 64 + lane;
-                const int ii = at >> 3, jj = (at & 7) * 4;
-                half4 h, l;
+        for (int it = 0; it < 4 * TI; ++it) {
+            const int at = it * 64 + lane;
+            const int ii = at >> 3, jj = (at & 7) * 4;
+            half4 h, l;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    _Float16 hh, ll;
-                    split_half(strip[(jj + e) * kPitch + ii], &hh, &ll);
-                    h[e] = hh;
-                    l[e] = ll;
+            for (int e = 0; e < 4; ++e) {
+                _Float16 hh, ll;
+                split_half(strip[(jj + e) * kPitch + ii], &hh, &ll);
+                h[e] = hh;
+                l[e] = ll;
+            }
+            _Float16* c = g.c + shift + (i0 + ii) * g.ldc + j0 + jj;
+            *reinterpret_cast<half4*>(c) = h;
+            if (SPLIT) *reinterpret_cast<half4*>(c + g.lo) = l;
+        }
+    }
+    wave_sync();
+}
+
+template <int V>
+struct Constant {
+    static constexpr int value = V;
+};
+
+// Waits until the wavefront's loads have landed and its LDS reads are done,
+// then for the other wavefronts of the block.
+__device__ __forceinline__ void arrive() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// C = P Q^T over tiles of 64 TI x 64 TJ, four wavefronts of 32 TI x 32 TJ each
+// (half the rows, half the columns).  Two stages of LDS, 64 columns of both
+// operands each, filled from global memory without passing registers.  (Small
+// tiles gained nothing from three or four stages, and lost the blocks per
+// compute unit that their LDS takes: 8 x 1024 x 1024, 444 us in all with two
+// stages, 460 with three, 512 with four.)
+template <int TI, int TJ, bool SPLIT, int KIND>
+__global__ __launch_bounds__(256, 1) void product_kernel(ProductArgs g) {
+    constexpr int BI = 64 * TI, BJ = 64 * TJ, kStages = 2;
+    __shared__ __attribute__((aligned(128))) _Float16 lds[kStages][(BI + BJ) * 64];
+    const int lane = lane_id(), wave = uniform(threadIdx.x >> 6);
+    const int wi = wave >> 1, wj = wave & 1;
+    const int tiles = symmetric(KIND) ? g.tiles_i * (g.tiles_i + 1) / 2 : g.tiles_i * g.tiles_j;
+    const int block = xcd_order(blockIdx.x, gridDim.x);
+    const int slice = block % g.slices, t = block / g.slices;
+    const int64_t matrix = t / tiles;
+    int ti, tj;
+    if (symmetric(KIND))
+        symmetric_tile(t % tiles, g.tiles_i, &ti, &tj);
+    else
+        full_tile(t % tiles, g.tiles_i, g.tiles_j, &ti, &tj);
+    const int64_t shift = matrix * (g.matrix_bytes / 2);
+    const int all = SPLIT ? 3 * g.k_steps : g.k_steps;
+    const int from = all * slice / g.slices, steps = all * (slice + 1) / g.slices - from;
+
+    // Loads: a wavefront instruction fills 8 rows of 64 elements.  The 16-byte
+    // piece c of row r sits at position c ^ (r / 2 & 7), so that the 16 lanes
+    // that read the LDS at once (one piece of 16 rows) meet all 64 banks.
+    const int lr = lane >> 3, lc = (lane & 7) ^ ((wave & 1) * 4 + (lr >> 1));
+    const _Float16* p = g.p + shift + ((int64_t)ti * BI + wave * 8 + lr) * g.ldp + lc * 8;
+    const _Float16* q = g.q + shift + ((int64_t)tj * BJ + wave * 8 + lr) * g.ldq + lc * 8;
+    constexpr int kLoads = 2 * (TI + TJ);  // of a wavefront for one stage
+    const int64_t hop_p = 32 * g.ldp, hop_q = 32 * g.ldq;
+    auto load = [&](int s, int l) {
+        _Float16* const stage = lds[s % kStages];
+        int64_t kp, kq;
+        if (SPLIT) {
+            const int k = (from + s) / 3, part = from + s - 3 * k;  // hi hi, hi lo, lo hi of the same columns
+            kp = (int64_t)k * 64 + (part == 2 ? g.lo : 0);
+            kq = (int64_t)k * 64 + (part == 1 ? g.lo : 0);
+        } else {
+            kp = kq = (int64_t)(from + s) * 64;
+        }
+        if (l < 2 * TI)
+            load_to_lds(p + (kp + l * hop_p), stage + (l * 32 + wave * 8) * 64);
+        else
+            load_to_lds(q + (kq + (l - 2 * TI) * hop_q), stage + BI * 64 + ((l - 2 * TI) * 32 + wave * 8) * 64);
+    };
+    // The 64 columns of a step are worked off in four quarters; the fragments
+    // of the next are read while the matrix cores work on the present one.
+    half8 fp[2][TI], fq[2][TJ];
+    constexpr int kReads = TI + TJ, kMul = TI * TJ;
+    const int row_p = wi * 32 * TI + (lane & 31), row_q = BI + wj * 32 * TJ + (lane & 31);
+    auto fetch = [&](int s, int quarter, int into, int k) {
+        const _Float16* const stage = lds[s % kStages];
+        const int pos = ((quarter * 2 + (lane >> 5)) ^ ((lane >> 1) & 7)) * 8;
+        if (k < TI)
+            fp[into][k] = *reinterpret_cast<const half8*>(stage + (row_p + k * 32) * 64 + pos);
+        else
+            fq[into][k - TI] = *reinterpret_cast<const half8*>(stage + (row_q + (k - TI) * 32) * 64 + pos);
+    };
+    float16v acc[TJ][TI];
+#pragma unroll
+    for (int b = 0; b < TJ; ++b)
+#pragma unroll
+        for (int a = 0; a < TI; ++a) acc[b][a] = 0.0f;
+    auto multiply = [&](int with, int first, int last) {
+#pragma unroll
+        for (int m = first; m < last; ++m) {
+            const int a = m / TJ, b = m % TJ;
+            acc[b][a] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fp[with][a], fq[with][b], acc[b][a], 0, 0, 0);
+        }
+    };
+    // A stage's loads go out as soon as it is free, in the last quarter of the
+    // step that used it; large tiles leave half of them to the next step's
+    // first two quarters, as one burst would hold up the products (8192 x
+    // 8192: 11.4 ms against 11.7).
+    constexpr bool kSpread = TI * TJ >= 8;
+    constexpr int kFirst = kSpread ? kLoads / 2 : kLoads, kSecond = kSpread ? kLoads * 3 / 4 : kLoads;
+    constexpr int kEarly = kSpread ? 4 : 0;  // products that cover the barrier
+    // MAIN: the step s + 2 exists.
+    auto step = [&](int s, auto main) {
+        constexpr bool kMain = main.value;
+#pragma unroll
+        for (int sub = 0; sub < 3; ++sub) {
+#pragma unroll
+            for (int k = 0; k < kReads; ++k) {
+                multiply(sub & 1, k * kMul / kReads, (k + 1) * kMul / kReads);
+                fetch(s, sub + 1, (sub + 1) & 1, k);
+                if (kSpread && (kMain || s + 1 < steps)) {
+                    const int l0 = sub == 0 ? kFirst : kSecond, n = sub == 0 ? kSecond - kFirst : sub == 1 ? kLoads - kSecond : 0;
+#pragma unroll
+                    for (int l = l0 + k * n / kReads; l < l0 + (k + 1) * n / kReads; ++l) load(s + 1, l);
                 }
-                _Float16* c = g.c + shift + (i0 + ii) * g.ldc + j0 + jb + jj;
-                *reinterpret_cast<half4*>(c) = h;
-                if (SPLIT) *reinterpret_cast<half4*>(c + g.lo) = l;
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
-        wave_sync();
+        // Every wavefront has its last fragments of this stage, and its own
+        // loads of the next one have landed: after the barrier that holds for
+        // all of them.
+        multiply(1, 0, kEarly);
+        __builtin_amdgcn_sched_barrier(0);
+        arrive();
+#pragma unroll
+        for (int k = 0; k < kReads; ++k) {
+            multiply(1, kEarly + k * (kMul - kEarly) / kReads, kEarly + (k + 1) * (kMul - kEarly) / kReads);
+            if (kMain || s + 1 < steps) fetch(s + 1, 0, 0, k);
+            if (kMain || s + 2 < steps)
+#pragma unroll
+                for (int l = k * kFirst / kReads; l < (k + 1) * kFirst / kReads; ++l) load(s + 2, l);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+#pragma unroll
+    for (int l = 0; l < kLoads; ++l) load(0, l);
+    arrive();
+    if (steps > 1)
+#pragma unroll
+        for (int l = 0; l < kFirst; ++l) load(1, l);
+#pragma unroll
+    for (int k = 0; k < kReads; ++k) fetch(0, 0, 0, k);
+    int s = 0;
+    for (; s + 2 < steps; ++s) step(s, Constant<1>{});
+    for (; s < steps; ++s) step(s, Constant<0>{});
+
+    if (symmetric(KIND) && g.slices > 1) {
+        float4* part = g.part + ((int64_t)t * g.slices + slice) * (TI * TJ * 4 * 256) + threadIdx.x;
+#pragma unroll
+        for (int b = 0; b < TJ; ++b)
+#pragma unroll
+            for (int a = 0; a < TI; ++a)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    part[((b * TI + a) * 4 + r) * 256] =
+                        make_float4(acc[b][a][r * 4], acc[b][a][r * 4 + 1], acc[b][a][r * 4 + 2], acc[b][a][r * 4 + 3]);
+        return;
     }
+    float* strip = reinterpret_cast<float*>(&lds[0][0]) + wave * ((BI + BJ) * 64 / 4);
+    static_assert(32 * strip_pitch(TI) <= (BI + BJ) * 64 / 4, "a strip fits a quarter of the LDS");
+#pragma unroll
+    for (int b = 0; b < TJ; ++b)
+        finish_strip<TI, SPLIT, KIND>(g, matrix, (int64_t)ti * BI + wi * 32 * TI, (int64_t)tj * BJ + wj * 32 * TJ + b * 32,
+                                      symmetric(KIND) && ti == tj, acc[b], strip);
+}
+
+// Joins the slices of a symmetric product: one wavefront for 32 columns of a
+// quarter tile, its slices' sums added in order.
+template <int T, bool SPLIT, int KIND>
+__global__ __launch_bounds__(64) void join_kernel(ProductArgs g) {
+    __shared__ __attribute__((aligned(16))) float strip[32 * strip_pitch(T)];
+    const int tiles = g.tiles_i * (g.tiles_i + 1) / 2;
+    const int b = blockIdx.x % T, wave = blockIdx.x / T % 4, t = blockIdx.x / (4 * T);
+    int ti, tj;
+    symmetric_tile(t % tiles, g.tiles_i, &ti, &tj);
+    const float4* part = g.part + (int64_t)t * g.slices * (T * T * 4 * 256) + b * T * 4 * 256 + wave * 64 + lane_id();
+    float16v acc[T];
+#pragma unroll
+    for (int a = 0; a < T; ++a) acc[a] = 0.0f;
+#pragma unroll 4
+    for (int s = 0; s < g.slices; ++s, part += T * T * 4 * 256)
+#pragma unroll
+        for (int a = 0; a < T; ++a)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float4 v = part[(a * 4 + r) * 256];
+                acc[a][r * 4] += v.x, acc[a][r * 4 + 1] += v.y, acc[a][r * 4 + 2] += v.z, acc[a][r * 4 + 3] += v.w;
+            }
+    finish_strip<T, SPLIT, KIND>(g, t / tiles, (int64_t)ti * 64 * T + (wave >> 1) * 32 * T,
+                                 (int64_t)tj * 64 * T + (wave & 1) * 32 * T + b * 32, ti == tj, acc, strip);
 }
 
 // ---------------------------------------------------------------------------
@@ -469,18 +595,36 @@ struct Plan {
     int64_t lo;            // elements between hi and lo arrays of one matrix
     int64_t x, xt0, xt1, a, b, da, db;  // byte offsets within one matrix's part
     int64_t matrix_bytes;
-    int64_t sums;          // byte offset of the partial sums
+    int64_t sums, part;    // byte offsets of the partial sums of squares and of sliced products
     int64_t total;
     int sum_blocks;
+    int gram_slices, poly_slices;
 };
 
+// Four consecutive elements of a row, from a multiple of four on, lie in one aligned word.
+bool aligned4(const MatrixView& v) {
+    return v.ld % 4 == 0 && v.stride % 4 == 0 && reinterpret_cast<uintptr_t>(v.ptr) % (4 * type_bytes(v.type)) == 0;
+}
+
 int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+// Slices of a symmetric product of `tiles` tiles and `steps` steps: enough
+// blocks to fill the chip, none shorter than 6 steps.
+int slices_of(int64_t tiles, int64_t steps, int tile) {
+    const int64_t room = tile == 4 ? 256 : tile == 2 ? 512 : 1024;  // blocks that run at once
+    const int64_t want = room / tiles, most = steps / 6;
+    return (int)(want < 2 || most < 2 ? 1 : want < most ? want : most);
+}
 
 Plan plan_of(int64_t rows, int64_t cols, int64_t count, bool split) {
     Plan p = {};
     const int64_t m = rows < cols ? rows : cols, n = rows < cols ? cols : rows;
     auto tiles = [&](int64_t t) { const int64_t k = (m + t - 1) / t; return count * k * (k + 1) / 2; };
-    p.tile = tiles(256) >= 192 ? 4 : tiles(128) >= 128 ? 2 : 1;
+    // Larger tiles do more products for each byte they read, smaller ones fill
+    // the chip with less work.  Measured in all (256 / 128 / 64): 4096 x 4096
+    // 1.85 / 1.95 / 2.42 ms; 8 x 1024 x 1024 625 / 420 / 442 us; 2048 x 2048
+    // 681 / 451 / 420 us, split 1250 / 841 / 982 us.
+    p.tile = tiles(256) >= 128 ? 4 : tiles(128) >= (split ? 36 : 160) ? 2 : 1;
     p.m = round_up(m, 64 * p.tile);
     p.n = round_up(n, 64 * p.tile);
     // All hi arrays, then all lo arrays in the same order.
@@ -501,8 +645,21 @@ Plan plan_of(int64_t rows, int64_t cols, int64_t count, bool split) {
     p.sums = count * at;
     const int64_t pieces = rows * ((cols + 2047) / 2048);
     p.sum_blocks = (int)(pieces < kSumBlocks ? pieces : kSumBlocks);
-    p.total = p.sums + round_up(count * p.sum_blocks * 8, 256);
+    p.part = p.sums + round_up(count * p.sum_blocks * 8, 256);
+    const int64_t sym = tiles(64 * p.tile), third = split ? 3 : 1;
+    p.gram_slices = slices_of(sym, third * p.n / 64, p.tile);
+    p.poly_slices = slices_of(sym, third * p.m / 64, p.tile);
+    const int64_t slices = p.gram_slices > p.poly_slices ? p.gram_slices : p.poly_slices;
+    p.total = p.part + (slices > 1 ? sym * slices * p.tile * p.tile * 4 * 256 * 16 : 0);
     return p;
+}
+
+template <int T, bool SPLIT, int KIND>
+void run_symmetric(ProductArgs g, int slices, int64_t count, hipStream_t stream) {
+    const unsigned tiles = (unsigned)(count * g.tiles_i * (g.tiles_i + 1) / 2);
+    g.slices = slices;
+    product_kernel<T, T, SPLIT, KIND><<<tiles * slices, 256, 0, stream>>>(g);
+    if (slices > 1) join_kernel<T, SPLIT, KIND><<<tiles * 4 * T, 64, 0, stream>>>(g);
 }
 
 template <int T, bool SPLIT>
@@ -514,7 +671,8 @@ hipError_t run_products(const UpdateArgs& u, const Plan& p, char* ws, hipStream_
     ProductArgs g = {};
     g.lo = p.lo;
     g.matrix_bytes = p.matrix_bytes;
-    const unsigned sym = (unsigned)(u.count * (tm * (tm + 1) / 2)), full = (unsigned)(u.count * tm * tn);
+    g.part = reinterpret_cast<float4*>(ws + p.part);
+    const unsigned full = (unsigned)(u.count * tm * tn);
     int64_t xt = p.xt0, xt_next = p.xt1;
     for (int s = 0; s < u.n_steps; ++s) {
         g.k = u.steps[s];
@@ -526,16 +684,17 @@ hipError_t run_products(const UpdateArgs& u, const Plan& p, char* ws, hipStream_
         g.ldc = g.ldct = p.m;
         g.diag_in = nullptr;
         g.diag_out = reinterpret_cast<float*>(ws + p.da);
-        product_kernel<T, SPLIT, kGram><<<sym, 256, 0, stream>>>(g);
+        run_symmetric<T, SPLIT, kGram>(g, p.gram_slices, u.count, stream);
         g.p = g.q = g.old = at(p.a);
         g.ldp = g.ldq = g.ldold = p.m;
         g.k_steps = (int)(p.m / 64);
         g.c = g.ct = at(p.b);
         g.diag_in = reinterpret_cast<const float*>(ws + p.da);
         g.diag_out = reinterpret_cast<float*>(ws + p.db);
-        product_kernel<T, SPLIT, kPoly><<<sym, 256, 0, stream>>>(g);
+        run_symmetric<T, SPLIT, kPoly>(g, p.poly_slices, u.count, stream);
         g.diag_in = reinterpret_cast<const float*>(ws + p.db);
         g.diag_out = nullptr;
+        g.slices = 1;
         if (s + 1 < u.n_steps) {
             g.tiles_j = tn;
             g.p = at(p.b);
@@ -543,7 +702,7 @@ hipError_t run_products(const UpdateArgs& u, const Plan& p, char* ws, hipStream_
             g.c = at(p.x);
             g.ldc = p.n;
             g.ct = at(xt_next);
-            product_kernel<T, SPLIT, kStep><<<full, 256, 0, stream>>>(g);
+            product_kernel<T, T, SPLIT, kStep><<<full, 256, 0, stream>>>(g);
             const int64_t was = xt;
             xt = xt_next;
             xt_next = was;
@@ -552,6 +711,7 @@ hipError_t run_products(const UpdateArgs& u, const Plan& p, char* ws, hipStream_
             g.out = u.out;
             g.out_i = u.cols;
             g.out_j = u.rows;
+            g.out_aligned = aligned4(u.out);
             g.update = u.momentum != nullptr;
             g.keep = u.keep;
             g.move = u.move;
@@ -562,7 +722,7 @@ hipError_t run_products(const UpdateArgs& u, const Plan& p, char* ws, hipStream_
             g.ldold = tall ? p.m : p.n;
             g.tiles_i = tall ? tm : tn;
             g.tiles_j = tall ? tn : tm;
-            product_kernel<T, SPLIT, kLast><<<full, 256, 0, stream>>>(g);
+            product_kernel<T, T, SPLIT, kLast><<<full, 256, 0, stream>>>(g);
         }
     }
     return hipGetLastError();
@@ -572,7 +732,13 @@ template <bool SPLIT>
 hipError_t run(const UpdateArgs& u, const Plan& p, char* ws, hipStream_t stream) {
     Source s = {u.x.ptr, u.x.type, u.x.ld, u.x.stride, u.momentum, u.grad_scale, u.decay, u.nesterov};
     double* sums = reinterpret_cast<double*>(ws + p.sums);
-    sum_squares_kernel<<<dim3(p.sum_blocks, (unsigned)u.count), 256, 0, stream>>>(s, u.rows, u.cols, sums);
+    const bool vector = u.cols % 8 == 0 && u.x.ld % 8 == 0 && u.x.stride % 8 == 0 &&
+                        reinterpret_cast<uintptr_t>(u.x.ptr) % 16 == 0;  // momentum is aligned and contiguous
+    const dim3 sum_grid(p.sum_blocks, (unsigned)u.count);
+    if (vector)
+        sum_squares_kernel<true><<<sum_grid, 256, 0, stream>>>(s, u.rows, u.cols, sums);
+    else
+        sum_squares_kernel<false><<<sum_grid, 256, 0, stream>>>(s, u.rows, u.cols, sums);
     const bool tall = u.rows > u.cols;
     const int64_t pr = tall ? p.n : p.m, pc = tall ? p.m : p.n;
     _Float16* direct = reinterpret_cast<_Float16*>(ws + (tall ? p.xt0 : p.x));
