@@ -23,44 +23,16 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "ops_internal.h"
-#include "types.h"
-#include "wave.h"
+#include "newton.h"
 
 namespace sl {
 namespace {
 
-typedef _Float16 half8 __attribute__((ext_vector_type(8)));
-typedef _Float16 half4 __attribute__((ext_vector_type(4)));
-typedef float float16v __attribute__((ext_vector_type(16)));
-
 constexpr float kScaleX = 8192.0f, kScaleA = 4096.0f, kScaleB = 2048.0f;
-constexpr int kSumBlocks = 1024;  // partial sums of squares per matrix, at most
+constexpr int kSumBlocks = 1024;  // of all matrices' partial sums of squares, about
 
 // ---------------------------------------------------------------------------
 // The start: sums of squares (with the momentum update), then X and X^T.
-
-// u of one element, before normalisation.
-struct Source {
-    const void* x;
-    int32_t type;
-    int64_t ld, stride;
-    float* momentum;  // null: u = x
-    float grad_scale, decay;
-    bool nesterov;
-};
-
-__device__ __forceinline__ float momentum_next(float g, float m, float decay) { return __builtin_fmaf(decay, m, g); }
-
-__device__ __forceinline__ double block_sum(double v, double* lds) {
-    for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
-    if (lane_id() == 0) lds[threadIdx.x >> 6] = v;
-    __syncthreads();
-    double s = 0;
-    for (int w = 0; w < (int)(blockDim.x >> 6); ++w) s += lds[w];
-    __syncthreads();
-    return s;
-}
 
 // partial[i * gridDim.x + block] = the block's share of matrix i's sum of u^2
 // in fp64 (no overflow or underflow for any finite fp32 values); momentum is
@@ -71,10 +43,10 @@ template <bool VECTOR>
 __global__ __launch_bounds__(256) void sum_squares_kernel(Source s, int64_t rows, int64_t cols, double* partial) {
     __shared__ double lds[4];
     const int64_t i = blockIdx.y;
-    const int pieces = (int)((cols + 2047) / 2048);
+    const int64_t pieces = (cols + 2047) / 2048;
     double acc = 0;
     for (int64_t t = blockIdx.x; t < rows * pieces; t += gridDim.x) {
-        const int64_t r = t / pieces;
+        const int64_t r = rows == 1 ? 0 : t / pieces;
         const int64_t c0 = (t - r * pieces) * 2048 + (VECTOR ? threadIdx.x * 8 : threadIdx.x);
         const int64_t at = i * s.stride + r * s.ld;
         float* m = s.momentum ? s.momentum + (i * rows + r) * cols : nullptr;
@@ -114,11 +86,6 @@ __global__ __launch_bounds__(256) void sum_squares_kernel(Source s, int64_t rows
     if (threadIdx.x == 0) partial[i * gridDim.x + blockIdx.x] = acc;
 }
 
-__device__ __forceinline__ void split_half(float v, _Float16* hi, _Float16* lo) {
-    *hi = (_Float16)v;
-    *lo = (_Float16)(v - (float)*hi);
-}
-
 // X = u * 2^13 / (|u| + eps) as fp16 (hi, and lo if split) in both
 // orientations, zero beyond the matrix: direct[r][c] (ld_direct) and
 // turned[c][r] (ld_turned), 64 x 64 elements per block.
@@ -144,16 +111,13 @@ __global__ __launch_bounds__(256) void start_kernel(Source s, int64_t rows, int6
             u[k] = s.nesterov ? __builtin_fmaf(s.decay, m, u[k] * s.grad_scale) : m;
         }
     }
-    double acc = 0;
-    for (int k = threadIdx.x; k < n_partial; k += 256) acc += partial[i * n_partial + k];
-    const double norm = sqrt(block_sum(acc, sums)) + (double)eps;
-    const double scale = norm > 0 ? (double)kScaleX / norm : 0;
+    const Scale scale = start_scale(kScaleX, partial, n_partial, i, eps, sums);
     direct = reinterpret_cast<_Float16*>(reinterpret_cast<char*>(direct) + i * matrix_bytes);
     turned = reinterpret_cast<_Float16*>(reinterpret_cast<char*>(turned) + i * matrix_bytes);
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
         const int r = tr + 4 * k;
-        const float v = (float)((double)u[k] * scale);
+        const float v = scale(u[k]);
         tile[r][tc] = v;
         _Float16 h, l;
         split_half(v, &h, &l);
@@ -202,15 +166,6 @@ struct ProductArgs {
     bool update;             // theta <- theta * keep - move * O
     float keep, move;
 };
-
-// Copies 16 bytes per lane from global memory to LDS, lane l's to lds + 16 l.
-// In assembler because the compiler makes later LDS reads wait for such copies
-// where it cannot tell the stages apart; arrive() waits for those that matter.  No register is
-// written, and m0 (the LDS address) needs one wait state before its use.
-__device__ __forceinline__ void load_to_lds(const _Float16* src, _Float16* lds) {
-    const uint32_t to = uniform((uint32_t)(uintptr_t)(__attribute__((address_space(3))) _Float16*)lds);
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(to) : "memory", "m0");
-}
 
 // Tile (ti, tj) of block t.  Symmetric products: the tiles with tj <= ti, in
 // groups of 4 tile rows taken column by column, so that the tiles in flight on
@@ -410,10 +365,6 @@ template <int V>
 struct Constant {
     static constexpr int value = V;
 };
-
-// Waits until the wavefront's loads have landed and its LDS reads are done,
-// then for the other wavefronts of the block.
-__device__ __forceinline__ void arrive() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 // C = P Q^T over tiles of 64 TI x 64 TJ, four wavefronts of 32 TI x 32 TJ each
 // (half the rows, half the columns).  Two stages of LDS, 64 columns of both
@@ -642,14 +593,18 @@ Plan plan_of(int64_t rows, int64_t cols, int64_t count, bool split) {
     p.db = at;
     at += round_up(p.m * 4, 256);
     p.matrix_bytes = at;
-    p.sums = count * at;
-    const int64_t pieces = rows * ((cols + 2047) / 2048);
-    p.sum_blocks = (int)(pieces < kSumBlocks ? pieces : kSumBlocks);
+    const int64_t narrow = !split && m <= kNarrow ? (int64_t)narrow_workspace_bytes(rows, cols, count) : 0;
+    p.sums = count * at > narrow ? count * at : narrow;
+    // A few pieces of 2048 elements for each block of the sums of squares, and
+    // few enough blocks that the next kernel adds them up in no time.
+    const int64_t pieces = (rows * cols + 2047) / 2048, most = round_up(kSumBlocks / count, 64);
+    p.sum_blocks = (int)(pieces < most ? pieces : most);
     p.part = p.sums + round_up(count * p.sum_blocks * 8, 256);
     const int64_t sym = tiles(64 * p.tile), third = split ? 3 : 1;
     p.gram_slices = slices_of(sym, third * p.n / 64, p.tile);
     p.poly_slices = slices_of(sym, third * p.m / 64, p.tile);
     const int64_t slices = p.gram_slices > p.poly_slices ? p.gram_slices : p.poly_slices;
+    // The sums of squares lie behind what either way needs.
     p.total = p.part + (slices > 1 ? sym * slices * p.tile * p.tile * 4 * 256 * 16 : 0);
     return p;
 }
@@ -732,13 +687,17 @@ template <bool SPLIT>
 hipError_t run(const UpdateArgs& u, const Plan& p, char* ws, hipStream_t stream) {
     Source s = {u.x.ptr, u.x.type, u.x.ld, u.x.stride, u.momentum, u.grad_scale, u.decay, u.nesterov};
     double* sums = reinterpret_cast<double*>(ws + p.sums);
-    const bool vector = u.cols % 8 == 0 && u.x.ld % 8 == 0 && u.x.stride % 8 == 0 &&
+    // Contiguous matrices are one long row.
+    const bool flat = u.x.ld == u.cols;
+    const int64_t sum_rows = flat ? 1 : u.rows, sum_cols = flat ? u.rows * u.cols : u.cols;
+    const bool vector = sum_cols % 8 == 0 && (flat || u.x.ld % 8 == 0) && u.x.stride % 8 == 0 &&
                         reinterpret_cast<uintptr_t>(u.x.ptr) % 16 == 0;  // momentum is aligned and contiguous
     const dim3 sum_grid(p.sum_blocks, (unsigned)u.count);
     if (vector)
-        sum_squares_kernel<true><<<sum_grid, 256, 0, stream>>>(s, u.rows, u.cols, sums);
+        sum_squares_kernel<true><<<sum_grid, 256, 0, stream>>>(s, sum_rows, sum_cols, sums);
     else
-        sum_squares_kernel<false><<<sum_grid, 256, 0, stream>>>(s, u.rows, u.cols, sums);
+        sum_squares_kernel<false><<<sum_grid, 256, 0, stream>>>(s, sum_rows, sum_cols, sums);
+    if (is_narrow(u)) return launch_narrow(u, s, sums, p.sum_blocks, ws, stream);
     const bool tall = u.rows > u.cols;
     const int64_t pr = tall ? p.n : p.m, pc = tall ? p.m : p.n;
     _Float16* direct = reinterpret_cast<_Float16*>(ws + (tall ? p.xt0 : p.x));

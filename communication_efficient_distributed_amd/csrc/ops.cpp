@@ -63,17 +63,30 @@ double largest_poly(double b, double c, double top) {
     return most;
 }
 
+// The largest |a + b q + c q^2| for q in [0, top].
+double largest_factor(double a, double b, double c, double top) {
+    auto f = [&](double q) { return std::fabs(a + b * q + c * q * q); };
+    double most = std::max(f(0), f(top));
+    if (c != 0 && -b / (2 * c) > 0 && -b / (2 * c) < top) most = std::max(most, f(-b / (2 * c)));
+    return most;
+}
+
 // Reads the steps and refuses those whose fp16 operands could overflow.
-sl_status read_steps(const float* coefficients, int32_t n, sl::Quintic* steps) {
+sl_status read_steps(const float* coefficients, int32_t n, sl::Quintic* steps, float* growth) {
     if (n < 1 || n > SL_MAX_STEPS || !coefficients) return SL_ERR_INVALID_ARG;
+    double product = 1, grown = 1;
     double top = 1.01;  // the start's largest singular value is at most 1, up to rounding
     for (int32_t k = 0; k < n; ++k) {
         const float a = coefficients[3 * k], b = coefficients[3 * k + 1], c = coefficients[3 * k + 2];
         if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return SL_ERR_INVALID_ARG;
         if (!(top <= 3.8) || !(largest_poly(b, c, top * top) <= 30)) return SL_ERR_INVALID_ARG;
+        const double factor = largest_factor(a, b, c, top * top);
+        product *= factor;
+        grown = std::max(grown, factor > 100 ? 1e30 : product);
         top = largest_value(a, b, c, top);
         steps[k] = {a, b, c};
     }
+    *growth = (float)std::min(grown, 1e30);
     return SL_OK;
 }
 
@@ -127,7 +140,8 @@ sl_status sl_orthogonalize(const void* x, int32_t x_type, int64_t x_ld, int64_t 
     if (st != SL_OK) return st;
     if (!known_type(x_type) || !known_type(out_type) || !std::isfinite(eps) || eps < 0) return SL_ERR_INVALID_ARG;
     sl::Quintic steps[SL_MAX_STEPS];
-    st = read_steps(coefficients, n_steps, steps);
+    float growth = 0;
+    st = read_steps(coefficients, n_steps, steps, &growth);
     if (st != SL_OK || noop) return st;
     if (!x || !out) return SL_ERR_INVALID_ARG;
     if (x_ld < cols || out_ld < cols) return SL_ERR_SHAPE;
@@ -146,7 +160,7 @@ sl_status sl_orthogonalize(const void* x, int32_t x_type, int64_t x_ld, int64_t 
     u.rows = rows, u.cols = cols, u.count = count;
     u.x = {const_cast<void*>(x), x_type, x_ld, x_stride};
     u.out = {out, out_type, out_ld, out_stride};
-    u.steps = steps, u.n_steps = n_steps, u.eps = eps, u.split = products == SL_PRODUCTS_SPLIT;
+    u.steps = steps, u.n_steps = n_steps, u.eps = eps, u.split = products == SL_PRODUCTS_SPLIT, u.growth = growth;
     return from_hip(sl::launch_update(u, workspace, static_cast<hipStream_t>(stream)));
 }
 
@@ -164,7 +178,8 @@ sl_status sl_muon_step(void* theta, int32_t theta_type, float* momentum, const v
     const float keep = (float)(1.0 - (double)lr * weight_decay), move = (float)((double)lr * update_scale);
     if (eps < 0 || !std::isfinite(keep) || !std::isfinite(move)) return SL_ERR_INVALID_ARG;
     sl::Quintic steps[SL_MAX_STEPS];
-    st = read_steps(coefficients, n_steps, steps);
+    float growth = 0;
+    st = read_steps(coefficients, n_steps, steps, &growth);
     if (st != SL_OK || noop) return st;
     if (!theta || !momentum || !grad) return SL_ERR_INVALID_ARG;
     if (!aligned(theta, 16) || !aligned(momentum, 16) || !aligned(grad, 16)) return SL_ERR_ALIGN;
@@ -185,7 +200,7 @@ sl_status sl_muon_step(void* theta, int32_t theta_type, float* momentum, const v
     u.grad_scale = grad_scale, u.decay = decay, u.nesterov = nesterov != 0;
     u.out = {theta, theta_type, cols, one};
     u.keep = keep, u.move = move;
-    u.steps = steps, u.n_steps = n_steps, u.eps = eps, u.split = products == SL_PRODUCTS_SPLIT;
+    u.steps = steps, u.n_steps = n_steps, u.eps = eps, u.split = products == SL_PRODUCTS_SPLIT, u.growth = growth;
     return from_hip(sl::launch_update(u, workspace, static_cast<hipStream_t>(stream)));
 }
 

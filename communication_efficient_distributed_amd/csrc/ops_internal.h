@@ -35,6 +35,9 @@ struct UpdateArgs {
     int32_t n_steps;
     float eps;
     bool split;           // products of values held as two fp16 terms
+    // The largest product of the first steps' factors |a + b q + c q^2| over the
+    // squared singular values q they can meet (1e30 if one factor passes 100).
+    float growth;
 };
 
 // Bytes of workspace launch_update needs.

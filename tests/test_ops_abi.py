@@ -167,7 +167,7 @@ def test_header_compiles_as_c99_and_links(lib, tmp_path):
     assert out.returncode == 0 and out.stdout.split() == ["OK"], (out.stdout, out.stderr)
 
 
-@pytest.mark.parametrize("source", ["newton.hip", "logprobs.hip"])
+@pytest.mark.parametrize("source", ["newton.hip", "newton_narrow.hip", "logprobs.hip"])
 def test_no_scratch_and_no_spills(source, tmp_path):
     spec = importlib.util.spec_from_file_location("resources", os.path.join(ROOT, "tests", "test_kernel_resources.py"))
     resources = importlib.util.module_from_spec(spec)
