@@ -138,8 +138,12 @@ __global__ __launch_bounds__(256) void start_kernel(Source s, int64_t rows, int6
 // ---------------------------------------------------------------------------
 // The products.
 
-enum { kGram, kPoly, kStep, kLast };
-constexpr bool symmetric(int kind) { return kind == kGram || kind == kPoly; }
+// C from the sums S = P Q^T: kGram A, kPoly B, kStep X, kLast the output; and
+// alpha S + beta old + gamma I: kSym symmetric, kFull (alpha S) in both
+// orientations, kEnd (alpha S) to the output.
+enum { kGram, kPoly, kStep, kLast, kSym, kFull, kEnd };
+constexpr bool symmetric(int kind) { return kind == kGram || kind == kPoly || kind == kSym; }
+constexpr bool to_output(int kind) { return kind == kLast || kind == kEnd; }
 
 struct ProductArgs {
     const _Float16 *p, *q;  // operands: rows of ldp / ldq elements along the summed index
@@ -158,6 +162,7 @@ struct ProductArgs {
     const float* diag_in;
     float* diag_out;
     Quintic k;
+    float alpha, beta, gamma;
     // last
     MatrixView out;
     int64_t out_i, out_j;    // extent of out along i (its columns) and j (its rows)
@@ -221,11 +226,13 @@ template <int TI, bool SPLIT, int KIND>
 __device__ __forceinline__ void finish_strip(const ProductArgs& g, int64_t matrix, int64_t i0, int64_t j0, bool on_diagonal,
                                              const float16v (&sums)[TI], float* strip) {
     constexpr int W = 32 * TI, kPitch = strip_pitch(TI);
-    constexpr int kTogether = 4 * TI < 8 ? 4 * TI : 8;  // loads in flight, within the register file
+    constexpr int kInFlight = 4 * TI < 8 ? 4 * TI : 8;  // loads in flight, within the register file
     const int lane = lane_id();
     const int64_t shift = matrix * (g.matrix_bytes / 2);
-    const float* diag_in = KIND == kGram ? nullptr : g.diag_in + matrix * (g.matrix_bytes / 4);
-    float* diag_out = symmetric(KIND) ? g.diag_out + matrix * (g.matrix_bytes / 4) : nullptr;
+    constexpr bool kDirect = KIND <= kLast;  // with the diagonals apart
+    const float* diag_in = KIND == kGram || !kDirect ? nullptr : g.diag_in + matrix * (g.matrix_bytes / 4);
+    float* diag_out = kDirect && symmetric(KIND) ? g.diag_out + matrix * (g.matrix_bytes / 4) : nullptr;
+    const bool has_old = KIND == kPoly || KIND == kStep || KIND == kLast || (KIND == kSym && g.old);
 #pragma unroll
     for (int a = 0; a < TI; ++a)
 #pragma unroll
@@ -235,11 +242,11 @@ __device__ __forceinline__ void finish_strip(const ProductArgs& g, int64_t matri
         }
     wave_sync();
 #pragma unroll 1
-    for (int it0 = 0; it0 < 4 * TI; it0 += kTogether) {
-        half4 oh[kTogether], ol[kTogether];
-        if (KIND != kGram) {
+    for (int it0 = 0; it0 < 4 * TI; it0 += kInFlight) {
+        half4 oh[kInFlight], ol[kInFlight];
+        if (has_old) {
 #pragma unroll
-            for (int it = 0; it < kTogether; ++it) {
+            for (int it = 0; it < kInFlight; ++it) {
                 const int at = (it0 + it) * 64 + lane;
                 const _Float16* old = g.old + shift + (j0 + at / (8 * TI)) * g.ldold + i0 + at % (8 * TI) * 4;
                 oh[it] = *reinterpret_cast<const half4*>(old);
@@ -247,18 +254,25 @@ __device__ __forceinline__ void finish_strip(const ProductArgs& g, int64_t matri
             }
         }
 #pragma unroll
-        for (int it = 0; it < kTogether; ++it) {
+        for (int it = 0; it < kInFlight; ++it) {
             const int at = (it0 + it) * 64 + lane;
             const int jj = at / (8 * TI), ii = at % (8 * TI) * 4;
             const int64_t i = i0 + ii, j = j0 + jj;
             float4* cell = reinterpret_cast<float4*>(&strip[jj * kPitch + ii]);
             const float4 sum = *cell;
             float v[4] = {sum.x, sum.y, sum.z, sum.w}, w[4];
-            if (KIND != kGram) {
+            if (has_old) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) w[e] = (float)oh[it][e] + (SPLIT ? (float)ol[it][e] : 0.0f);
             }
-            if (KIND == kGram) {
+            if (!kDirect) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    v[e] *= g.alpha;
+                    if (KIND == kSym && has_old) v[e] = __builtin_fmaf(g.beta, w[e], v[e]);
+                    if (KIND == kSym && i + e == j) v[e] += g.gamma;
+                }
+            } else if (KIND == kGram) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     if (i + e == j) {
@@ -292,9 +306,10 @@ __device__ __forceinline__ void finish_strip(const ProductArgs& g, int64_t matri
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] = (g.k.a + dd[e]) * w[e] + v[e] * (1.0f / kScaleB);  // times kScaleX
             }
-            if (KIND == kLast) {
+            if (to_output(KIND)) {
+                if (KIND == kLast)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] *= 1.0f / kScaleX;
+                    for (int e = 0; e < 4; ++e) v[e] *= 1.0f / kScaleX;
                 if (g.out_aligned && i + 4 <= g.out_i) {
                     if (j < g.out_j) {
                         const int64_t to = matrix * g.out.stride + j * g.out.ld + i;
@@ -325,7 +340,7 @@ __device__ __forceinline__ void finish_strip(const ProductArgs& g, int64_t matri
         }
     }
     wave_sync();
-    if (KIND == kLast) {
+    if (to_output(KIND)) {
         // What four at once did not reach: consecutive i, one element per lane.
         const int64_t done = g.out_aligned ? g.out_i & ~(int64_t)3 : 0;
         if (i0 + W > done)
@@ -491,7 +506,7 @@ __global__ __launch_bounds__(256, 1) void product_kernel(ProductArgs g) {
     for (; s + 2 < steps; ++s) step(s, Constant<1>{});
     for (; s < steps; ++s) step(s, Constant<0>{});
 
-    if (symmetric(KIND) && g.slices > 1) {
+    if (TI < 4 && symmetric(KIND) && g.slices > 1) {
         float4* part = g.part + ((int64_t)t * g.slices + slice) * (TI * TJ * 4 * 256) + threadIdx.x;
 #pragma unroll
         for (int b = 0; b < TJ; ++b)
@@ -545,6 +560,8 @@ struct Plan {
     int64_t m, n;          // padded to the tile
     int64_t lo;            // elements between hi and lo arrays of one matrix
     int64_t x, xt0, xt1, a, b, da, db;  // byte offsets within one matrix's part
+    bool by_gram;          // room for that way, with three more square matrices
+    int64_t c[3];
     int64_t matrix_bytes;
     int64_t sums, part;    // byte offsets of the partial sums of squares and of sliced products
     int64_t total;
@@ -562,12 +579,13 @@ int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 // Slices of a symmetric product of `tiles` tiles and `steps` steps: enough
 // blocks to fill the chip, none shorter than 6 steps.
 int slices_of(int64_t tiles, int64_t steps, int tile) {
-    const int64_t room = tile == 4 ? 256 : tile == 2 ? 512 : 1024;  // blocks that run at once
+    if (tile == 4) return 1;
+    const int64_t room = tile == 2 ? 512 : 1024;  // blocks that run at once
     const int64_t want = room / tiles, most = steps / 6;
     return (int)(want < 2 || most < 2 ? 1 : want < most ? want : most);
 }
 
-Plan plan_of(int64_t rows, int64_t cols, int64_t count, bool split) {
+Plan plan_of(int64_t rows, int64_t cols, int64_t count, bool split, bool update) {
     Plan p = {};
     const int64_t m = rows < cols ? rows : cols, n = rows < cols ? cols : rows;
     auto tiles = [&](int64_t t) { const int64_t k = (m + t - 1) / t; return count * k * (k + 1) / 2; };
@@ -586,6 +604,10 @@ Plan plan_of(int64_t rows, int64_t cols, int64_t count, bool split) {
     p.xt1 = take(p.m * p.n);
     p.a = take(p.m * p.m);
     p.b = take(p.m * p.m);
+    // The products of square matrices have to be large enough to run at full rate.
+    p.by_gram = update && split && p.tile == 4 && 2 * n >= 3 * m;
+    if (p.by_gram)
+        for (int64_t& c : p.c) c = take(p.m * p.m);
     p.lo = at / 2;
     if (split) at *= 2;
     p.da = at;
@@ -614,7 +636,8 @@ void run_symmetric(ProductArgs g, int slices, int64_t count, hipStream_t stream)
     const unsigned tiles = (unsigned)(count * g.tiles_i * (g.tiles_i + 1) / 2);
     g.slices = slices;
     product_kernel<T, T, SPLIT, KIND><<<tiles * slices, 256, 0, stream>>>(g);
-    if (slices > 1) join_kernel<T, SPLIT, KIND><<<tiles * 4 * T, 64, 0, stream>>>(g);
+    if constexpr (T < 4)  // where the largest tiles are taken there are enough of them
+        if (slices > 1) join_kernel<T, SPLIT, KIND><<<tiles * 4 * T, 64, 0, stream>>>(g);
 }
 
 template <int T, bool SPLIT>
@@ -683,6 +706,108 @@ hipError_t run_products(const UpdateArgs& u, const Plan& p, char* ws, hipStream_
     return hipGetLastError();
 }
 
+// Steps between two Gram matrices of X, and how much Q may grow over them.
+constexpr int kTogether = 3;
+constexpr float kMaxGrowth = 256.0f;
+
+// |Q|'s bound over the steps from `from` on, up to kTogether of them.
+float growth_of(const UpdateArgs& u, int from) {
+    float most = 1, product = 1;
+    for (int s = from; s < u.n_steps && s < from + kTogether; ++s) {
+        product *= u.factors[s];
+        if (product > most) most = product;
+        if (u.factors[s] > most) most = u.factors[s];
+    }
+    return most;
+}
+
+hipError_t run_by_gram(const UpdateArgs& u, const Plan& p, char* ws, hipStream_t stream) {
+    constexpr float kScaleR = 2048.0f;  // |R| and |P R| are at most 3.8^2
+    const bool tall = u.rows > u.cols;
+    const int tm = (int)(p.m / 256), tn = (int)(p.n / 256);
+    auto at = [&](int64_t o) { return reinterpret_cast<_Float16*>(ws + o); };
+    ProductArgs g = {};
+    g.lo = p.lo;
+    g.matrix_bytes = p.matrix_bytes;
+    g.slices = 1;
+    const unsigned sym = (unsigned)(u.count * (tm * (tm + 1) / 2)), full = (unsigned)(u.count * tm * tn);
+    // to = alpha a b + beta old + gamma I, all m x m.
+    auto square = [&](int64_t to, int64_t a, int64_t b, float alpha, int64_t old, float beta, float gamma) {
+        g.tiles_i = g.tiles_j = tm;
+        g.p = at(a), g.q = at(b);
+        g.ldp = g.ldq = g.ldold = g.ldc = g.ldct = p.m;
+        g.k_steps = (int)(p.m / 64);
+        g.old = old < 0 ? nullptr : at(old);
+        g.c = g.ct = at(to);
+        g.alpha = alpha, g.beta = beta, g.gamma = gamma;
+        product_kernel<4, 4, true, kSym><<<sym, 256, 0, stream>>>(g);
+    };
+    const int64_t r = p.a, t = p.b;
+    int64_t xt = p.xt0, xt_next = p.xt1;
+    for (int from = 0; from < u.n_steps; from += kTogether) {
+        const int to = from + kTogether < u.n_steps ? from + kTogether : u.n_steps;
+        float scale = 16384.0f;  // of P and Q
+        for (float f = 1; f < growth_of(u, from); f *= 2) scale *= 0.5f;
+        g.tiles_i = g.tiles_j = tm;
+        g.p = g.q = at(p.x);
+        g.ldp = g.ldq = p.n;
+        g.ldc = g.ldct = p.m;
+        g.k_steps = (int)(p.n / 64);
+        g.old = nullptr;
+        g.c = g.ct = at(r);
+        g.alpha = kScaleR / (kScaleX * kScaleX), g.beta = g.gamma = 0;
+        product_kernel<4, 4, true, kSym><<<sym, 256, 0, stream>>>(g);
+        int64_t poly = p.c[0], q = p.c[1], q_next = p.c[2];
+        for (int s = from; s < to; ++s) {
+            const Quintic& k = u.steps[s];
+            square(poly, r, r, k.c * scale / (kScaleR * kScaleR), r, k.b * scale / kScaleR, k.a * scale);
+            if (s + 1 < to) {
+                square(t, poly, r, 1 / scale, -1, 0, 0);
+                square(r, t, poly, 1 / scale, -1, 0, 0);
+            }
+            if (s == from) {
+                const int64_t was = q;
+                q = poly;
+                poly = was;
+            } else {
+                square(q_next, q, poly, 1 / scale, -1, 0, 0);
+                const int64_t was = q;
+                q = q_next;
+                q_next = was;
+            }
+        }
+        g.old = nullptr;
+        g.k_steps = (int)(p.m / 64);
+        g.ldp = g.ldq = p.m;
+        if (to < u.n_steps) {
+            g.tiles_i = tm, g.tiles_j = tn;
+            g.p = at(q), g.q = at(xt);
+            g.c = at(p.x), g.ldc = p.n;
+            g.ct = at(xt_next), g.ldct = p.m;
+            g.alpha = 1 / scale;
+            product_kernel<4, 4, true, kFull><<<full, 256, 0, stream>>>(g);
+            const int64_t was = xt;
+            xt = xt_next;
+            xt_next = was;
+        } else {
+            g.out = u.out;
+            g.out_i = u.cols;
+            g.out_j = u.rows;
+            g.out_aligned = aligned4(u.out);
+            g.update = u.momentum != nullptr;
+            g.keep = u.keep;
+            g.move = u.move;
+            g.alpha = 1 / (scale * kScaleX);
+            g.p = at(tall ? q : xt);
+            g.q = at(tall ? xt : q);
+            g.tiles_i = tall ? tm : tn;
+            g.tiles_j = tall ? tn : tm;
+            product_kernel<4, 4, true, kEnd><<<full, 256, 0, stream>>>(g);
+        }
+    }
+    return hipGetLastError();
+}
+
 template <bool SPLIT>
 hipError_t run(const UpdateArgs& u, const Plan& p, char* ws, hipStream_t stream) {
     Source s = {u.x.ptr, u.x.type, u.x.ld, u.x.stride, u.momentum, u.grad_scale, u.decay, u.nesterov};
@@ -704,6 +829,11 @@ hipError_t run(const UpdateArgs& u, const Plan& p, char* ws, hipStream_t stream)
     _Float16* turned = reinterpret_cast<_Float16*>(ws + (tall ? p.x : p.xt0));
     start_kernel<SPLIT><<<dim3((unsigned)(pc / 64), (unsigned)(pr / 64), (unsigned)u.count), 256, 0, stream>>>(
         s, u.rows, u.cols, sums, p.sum_blocks, u.eps, direct, pc, turned, pr, p.lo, p.matrix_bytes);
+    if (p.by_gram) {
+        float most = 0;
+        for (int from = 0; from < u.n_steps; from += kTogether) most = fmaxf(most, growth_of(u, from));
+        if (most <= kMaxGrowth) return run_by_gram(u, p, ws, stream);
+    }
     if (p.tile == 4) return run_products<4, SPLIT>(u, p, ws, stream);
     if (p.tile == 2) return run_products<2, SPLIT>(u, p, ws, stream);
     return run_products<1, SPLIT>(u, p, ws, stream);
@@ -711,12 +841,12 @@ hipError_t run(const UpdateArgs& u, const Plan& p, char* ws, hipStream_t stream)
 
 }  // namespace
 
-size_t update_workspace_bytes(int64_t rows, int64_t cols, int64_t count, bool split) {
-    return (size_t)plan_of(rows, cols, count, split).total;
+size_t update_workspace_bytes(int64_t rows, int64_t cols, int64_t count, bool split, bool update) {
+    return (size_t)plan_of(rows, cols, count, split, update).total;
 }
 
 hipError_t launch_update(const UpdateArgs& u, void* workspace, hipStream_t stream) {
-    const Plan p = plan_of(u.rows, u.cols, u.count, u.split);
+    const Plan p = plan_of(u.rows, u.cols, u.count, u.split, u.momentum != nullptr);
     char* ws = static_cast<char*>(workspace);
     return u.split ? run<true>(u, p, ws, stream) : run<false>(u, p, ws, stream);
 }

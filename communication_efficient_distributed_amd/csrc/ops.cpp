@@ -72,7 +72,7 @@ double largest_factor(double a, double b, double c, double top) {
 }
 
 // Reads the steps and refuses those whose fp16 operands could overflow.
-sl_status read_steps(const float* coefficients, int32_t n, sl::Quintic* steps, float* growth) {
+sl_status read_steps(const float* coefficients, int32_t n, sl::Quintic* steps, sl::UpdateArgs* u) {
     if (n < 1 || n > SL_MAX_STEPS || !coefficients) return SL_ERR_INVALID_ARG;
     double product = 1, grown = 1;
     double top = 1.01;  // the start's largest singular value is at most 1, up to rounding
@@ -82,11 +82,12 @@ sl_status read_steps(const float* coefficients, int32_t n, sl::Quintic* steps, f
         if (!(top <= 3.8) || !(largest_poly(b, c, top * top) <= 30)) return SL_ERR_INVALID_ARG;
         const double factor = largest_factor(a, b, c, top * top);
         product *= factor;
+        u->factors[k] = (float)std::min(factor, 1e30);
         grown = std::max(grown, factor > 100 ? 1e30 : product);
         top = largest_value(a, b, c, top);
         steps[k] = {a, b, c};
     }
-    *growth = (float)std::min(grown, 1e30);
+    u->growth = (float)std::min(grown, 1e30);
     return SL_OK;
 }
 
@@ -107,10 +108,10 @@ sl_status check_sizes(int64_t rows, int64_t cols, int64_t count, int32_t product
     return SL_OK;
 }
 
-int64_t update_workspace(int64_t rows, int64_t cols, int64_t count, int32_t products) {
+int64_t update_workspace(int64_t rows, int64_t cols, int64_t count, int32_t products, bool update) {
     bool noop = false;
     if (check_sizes(rows, cols, count, products, &noop) != SL_OK) return -1;
-    return noop ? 0 : (int64_t)sl::update_workspace_bytes(rows, cols, count, products == SL_PRODUCTS_SPLIT);
+    return noop ? 0 : (int64_t)sl::update_workspace_bytes(rows, cols, count, products == SL_PRODUCTS_SPLIT, update);
 }
 
 sl_status check_workspace(const void* workspace, int64_t bytes, int64_t need) {
@@ -124,11 +125,11 @@ sl_status check_workspace(const void* workspace, int64_t bytes, int64_t need) {
 extern "C" {
 
 int64_t sl_orthogonalize_workspace(int64_t rows, int64_t cols, int64_t count, int32_t products) {
-    return update_workspace(rows, cols, count, products);
+    return update_workspace(rows, cols, count, products, false);
 }
 
 int64_t sl_muon_step_workspace(int64_t rows, int64_t cols, int64_t count, int32_t products) {
-    return update_workspace(rows, cols, count, products);
+    return update_workspace(rows, cols, count, products, true);
 }
 
 sl_status sl_orthogonalize(const void* x, int32_t x_type, int64_t x_ld, int64_t x_stride, void* out,
@@ -140,8 +141,8 @@ sl_status sl_orthogonalize(const void* x, int32_t x_type, int64_t x_ld, int64_t 
     if (st != SL_OK) return st;
     if (!known_type(x_type) || !known_type(out_type) || !std::isfinite(eps) || eps < 0) return SL_ERR_INVALID_ARG;
     sl::Quintic steps[SL_MAX_STEPS];
-    float growth = 0;
-    st = read_steps(coefficients, n_steps, steps, &growth);
+    sl::UpdateArgs u = {};
+    st = read_steps(coefficients, n_steps, steps, &u);
     if (st != SL_OK || noop) return st;
     if (!x || !out) return SL_ERR_INVALID_ARG;
     if (x_ld < cols || out_ld < cols) return SL_ERR_SHAPE;
@@ -150,17 +151,16 @@ sl_status sl_orthogonalize(const void* x, int32_t x_type, int64_t x_ld, int64_t 
     const int64_t nx = extent(rows, cols, count, x_ld, x_stride), no = extent(rows, cols, count, out_ld, out_stride);
     if (nx < 0 || no < 0) return SL_ERR_SHAPE;
     if (!aligned(x, bytes_of(x_type)) || !aligned(out, bytes_of(out_type))) return SL_ERR_ALIGN;
-    const int64_t need = update_workspace(rows, cols, count, products);
+    const int64_t need = update_workspace(rows, cols, count, products, false);
     st = check_workspace(workspace, workspace_bytes, need);
     if (st != SL_OK) return st;
     const size_t bx = nx * bytes_of(x_type), bo = no * bytes_of(out_type);
     if (overlap(x, bx, out, bo) || overlap(workspace, need, x, bx) || overlap(workspace, need, out, bo))
         return SL_ERR_INVALID_ARG;
-    sl::UpdateArgs u = {};
     u.rows = rows, u.cols = cols, u.count = count;
     u.x = {const_cast<void*>(x), x_type, x_ld, x_stride};
     u.out = {out, out_type, out_ld, out_stride};
-    u.steps = steps, u.n_steps = n_steps, u.eps = eps, u.split = products == SL_PRODUCTS_SPLIT, u.growth = growth;
+    u.steps = steps, u.n_steps = n_steps, u.eps = eps, u.split = products == SL_PRODUCTS_SPLIT;
     return from_hip(sl::launch_update(u, workspace, static_cast<hipStream_t>(stream)));
 }
 
@@ -178,12 +178,12 @@ sl_status sl_muon_step(void* theta, int32_t theta_type, float* momentum, const v
     const float keep = (float)(1.0 - (double)lr * weight_decay), move = (float)((double)lr * update_scale);
     if (eps < 0 || !std::isfinite(keep) || !std::isfinite(move)) return SL_ERR_INVALID_ARG;
     sl::Quintic steps[SL_MAX_STEPS];
-    float growth = 0;
-    st = read_steps(coefficients, n_steps, steps, &growth);
+    sl::UpdateArgs u = {};
+    st = read_steps(coefficients, n_steps, steps, &u);
     if (st != SL_OK || noop) return st;
     if (!theta || !momentum || !grad) return SL_ERR_INVALID_ARG;
     if (!aligned(theta, 16) || !aligned(momentum, 16) || !aligned(grad, 16)) return SL_ERR_ALIGN;
-    const int64_t need = update_workspace(rows, cols, count, products);
+    const int64_t need = update_workspace(rows, cols, count, products, true);
     st = check_workspace(workspace, workspace_bytes, need);
     if (st != SL_OK) return st;
     const int64_t one = rows * cols;
@@ -193,14 +193,13 @@ sl_status sl_muon_step(void* theta, int32_t theta_type, float* momentum, const v
     for (int a = 0; a < 4; ++a)
         for (int b = 0; b < a; ++b)
             if (overlap(bufs[a], lens[a], bufs[b], lens[b])) return SL_ERR_INVALID_ARG;
-    sl::UpdateArgs u = {};
     u.rows = rows, u.cols = cols, u.count = count;
     u.x = {const_cast<void*>(grad), grad_type, cols, one};
     u.momentum = momentum;
     u.grad_scale = grad_scale, u.decay = decay, u.nesterov = nesterov != 0;
     u.out = {theta, theta_type, cols, one};
     u.keep = keep, u.move = move;
-    u.steps = steps, u.n_steps = n_steps, u.eps = eps, u.split = products == SL_PRODUCTS_SPLIT, u.growth = growth;
+    u.steps = steps, u.n_steps = n_steps, u.eps = eps, u.split = products == SL_PRODUCTS_SPLIT;
     return from_hip(sl::launch_update(u, workspace, static_cast<hipStream_t>(stream)));
 }
 

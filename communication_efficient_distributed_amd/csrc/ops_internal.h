@@ -38,10 +38,12 @@ struct UpdateArgs {
     // The largest product of the first steps' factors |a + b q + c q^2| over the
     // squared singular values q they can meet (1e30 if one factor passes 100).
     float growth;
+    float factors[SL_MAX_STEPS];  // each step's own
 };
 
 // Bytes of workspace launch_update needs.
-size_t update_workspace_bytes(int64_t rows, int64_t cols, int64_t count, bool split);
+// (update: for sl_muon_step.)
+size_t update_workspace_bytes(int64_t rows, int64_t cols, int64_t count, bool split, bool update);
 hipError_t launch_update(const UpdateArgs& u, void* workspace, hipStream_t stream);
 
 struct LogprobArgs {

@@ -195,6 +195,37 @@ def test_muon_step(theta_dtype, grad_dtype, products, nesterov, count, rows, col
         assert off <= move * (tol + 64 * 2.0 ** -24) + rounding
 
 
+@pytest.mark.parametrize("rows,cols", [(1800, 2701), (2703, 1799)])
+def test_muon_step_of_large_matrices_by_their_gram_matrix(rows, cols):
+    """Split operands, large, one side 1.5 times the other: three steps at a time on the Gram matrix.  An error of
+    22 bits in R is stretched, where R's eigenvalues are smallest, by the square of a step's largest factor 3.4445
+    for each of the two steps that follow: 141 * 2^-22 / 3 = 1.1e-5 if every eigenvalue were that small (a third of
+    them, say), in each of the two runs of steps."""
+    sl = require_gpu()
+    note(f"muon by gram {rows}x{cols}")
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    grad = torch.randn((4, rows, cols), generator=g, device="cuda")
+    grad *= torch.randn((4, rows, 1), generator=g, device="cuda").exp()
+    theta, momentum = torch.zeros_like(grad), torch.zeros_like(grad)
+    sl.muon_step(theta, momentum, grad, lr=1.0, nesterov=False, products="split")
+    assert torch.equal(momentum, grad)
+    for k in (0, 3):
+        err = relative(-theta[k], newton_schulz(grad[k]))
+        assert err <= 2 * 1.1e-5, err
+    # four steps end in a run of one; momentum is momentum * 0.95 + grad by now
+    theta.zero_()
+    sl.muon_step(theta, momentum, grad, lr=1.0, nesterov=False, products="split", coefficients=STEPS[:4])
+    err = relative(-theta[1], newton_schulz(momentum[1], STEPS[:4]))
+    assert err <= 2 * 1.1e-5, err
+    # steps that let Q grow past what fp16 pairs should carry take the other way
+    steps = ((3.7, -5.3, 2.2), (8.0, -14.0, 6.0), (9.0, -8.0, 1.2))
+    theta.zero_()
+    sl.muon_step(theta, momentum, grad, lr=1.0, nesterov=False, products="split", coefficients=steps)
+    want = newton_schulz(momentum[2], steps)
+    tol = newton_schulz_tolerance(momentum[2], want, True, steps)
+    assert relative(-theta[2], want) <= tol
+
+
 def test_muon_step_is_the_composition():
     """theta's move is what sl_orthogonalize gives for the same u: bitwise with keep 1 and move 1 from zero weights."""
     sl = require_gpu()

@@ -112,7 +112,10 @@ def test_workspace_sizes(lib):
         one, split = f(8192, 28672, 1, 0), f(8192, 28672, 1, 1)
         # three copies of X and two square matrices, twice for split operands; little else
         operands = 2 * (3 * 8192 * 28672 + 2 * 8192 * 8192)
-        assert operands <= one <= 1.1 * operands and 2 * operands <= split <= 2.2 * operands
+        assert operands <= one <= 1.1 * operands
+        # the weight update keeps three more square matrices at this shape
+        more = 3 * 4 * 8192 * 8192 if f is lib.sl_muon_step_workspace else 0
+        assert 2 * operands + more <= split <= 2.2 * operands + more
         assert f(28672, 8192, 1, 0) == one and 3 * one // 4 < f(8192, 28672, 4, 0) // 4 <= one + 4096
     f = lib.sl_token_logprobs_workspace
     assert f(0, 10, 0, 0) == 0 and f(4, 0, 0, 0) == f(4, 10, 7, 0) == f(4, 10, 0, 33) == f(-1, 10, 0, 0) == -1
