@@ -376,6 +376,8 @@ __device__ __forceinline__ void finish_strip(const ProductArgs& g, int64_t matri
     wave_sync();
 }
 
+enum { kPlain, kInTurn, kPaired };
+
 template <int V>
 struct Constant {
     static constexpr int value = V;
@@ -383,12 +385,19 @@ struct Constant {
 
 // C = P Q^T over tiles of 64 TI x 64 TJ, four wavefronts of 32 TI x 32 TJ each
 // (half the rows, half the columns).  Two stages of LDS, 64 columns of both
-// operands each, filled from global memory without passing registers.  (Small
+// operands each, filled from global memory without passing registers.  Split
+// operands (TERMS) take the three products of the same columns one after
+// another, or 32 columns of hi and of lo at a time and all three from those:
+// less LDS traffic, but half lines from memory.  Measured on whole calls: one
+// 1024 x 1024 409 against 345 us, three 1000 x 2731 867 against 830; but the
+// Gram matrix of 1024 x 8192 35 against 45 us, and 256 x 256 tiles (8192 x
+// 28672) 55.5 against 57.5 ms.  So: pairs for small tiles along the short side.  (Small
 // tiles gained nothing from three or four stages, and lost the blocks per
 // compute unit that their LDS takes: 8 x 1024 x 1024, 444 us in all with two
 // stages, 460 with three, 512 with four.)
-template <int TI, int TJ, bool SPLIT, int KIND>
+template <int TI, int TJ, int TERMS, int KIND>
 __global__ __launch_bounds__(256, 1) void product_kernel(ProductArgs g) {
+    constexpr bool SPLIT = TERMS != kPlain, PAIRED = TERMS == kPaired;
     constexpr int BI = 64 * TI, BJ = 64 * TJ, kStages = 2;
     __shared__ __attribute__((aligned(128))) _Float16 lds[kStages][(BI + BJ) * 64];
     const int lane = lane_id(), wave = uniform(threadIdx.x >> 6);
@@ -403,44 +412,47 @@ __global__ __launch_bounds__(256, 1) void product_kernel(ProductArgs g) {
     else
         full_tile(t % tiles, g.tiles_i, g.tiles_j, &ti, &tj);
     const int64_t shift = matrix * (g.matrix_bytes / 2);
-    const int all = SPLIT ? 3 * g.k_steps : g.k_steps;
+    const int all = g.k_steps * (PAIRED ? 2 : SPLIT ? 3 : 1);
     const int from = all * slice / g.slices, steps = all * (slice + 1) / g.slices - from;
 
     // Loads: a wavefront instruction fills 8 rows of 64 elements.  The 16-byte
     // piece c of row r sits at position c ^ (r / 2 & 7), so that the 16 lanes
     // that read the LDS at once (one piece of 16 rows) meet all 64 banks.
     const int lr = lane >> 3, lc = (lane & 7) ^ ((wave & 1) * 4 + (lr >> 1));
-    const _Float16* p = g.p + shift + ((int64_t)ti * BI + wave * 8 + lr) * g.ldp + lc * 8;
-    const _Float16* q = g.q + shift + ((int64_t)tj * BJ + wave * 8 + lr) * g.ldq + lc * 8;
+    const int64_t piece = PAIRED ? (lc & 3) * 8 + (lc >> 2) * g.lo : lc * 8;  // pieces 0 to 3 of hi, then of lo
+    const _Float16* p = g.p + shift + ((int64_t)ti * BI + wave * 8 + lr) * g.ldp + piece;
+    const _Float16* q = g.q + shift + ((int64_t)tj * BJ + wave * 8 + lr) * g.ldq + piece;
     constexpr int kLoads = 2 * (TI + TJ);  // of a wavefront for one stage
     const int64_t hop_p = 32 * g.ldp, hop_q = 32 * g.ldq;
     auto load = [&](int s, int l) {
         _Float16* const stage = lds[s % kStages];
         int64_t kp, kq;
-        if (SPLIT) {
-            const int k = (from + s) / 3, part = from + s - 3 * k;  // hi hi, hi lo, lo hi of the same columns
-            kp = (int64_t)k * 64 + (part == 2 ? g.lo : 0);
-            kq = (int64_t)k * 64 + (part == 1 ? g.lo : 0);
+        if (SPLIT && !PAIRED) {
+            const int k = (from + s) / 3, term = from + s - 3 * k;  // hi hi, hi lo, lo hi of the same columns
+            kp = (int64_t)k * 64 + (term == 2 ? g.lo : 0);
+            kq = (int64_t)k * 64 + (term == 1 ? g.lo : 0);
         } else {
-            kp = kq = (int64_t)(from + s) * 64;
+            kp = kq = (int64_t)(from + s) * (PAIRED ? 32 : 64);
         }
         if (l < 2 * TI)
             load_to_lds(p + (kp + l * hop_p), stage + (l * 32 + wave * 8) * 64);
         else
             load_to_lds(q + (kq + (l - 2 * TI) * hop_q), stage + BI * 64 + ((l - 2 * TI) * 32 + wave * 8) * 64);
     };
-    // The 64 columns of a step are worked off in four quarters; the fragments
-    // of the next are read while the matrix cores work on the present one.
-    half8 fp[2][TI], fq[2][TJ];
-    constexpr int kReads = TI + TJ, kMul = TI * TJ;
+    // A step is worked off 16 columns at a time; the fragments of the next 16
+    // are read while the matrix cores work on the present ones.
+    constexpr int kParts = PAIRED ? 2 : 4, kPair = PAIRED ? 2 : 1;
+    half8 fp[2][kPair][TI], fq[2][kPair][TJ];
+    constexpr int kReads = kPair * (TI + TJ), kMul = (PAIRED ? 3 : 1) * TI * TJ;
     const int row_p = wi * 32 * TI + (lane & 31), row_q = BI + wj * 32 * TJ + (lane & 31);
-    auto fetch = [&](int s, int quarter, int into, int k) {
+    auto fetch = [&](int s, int part, int into, int k) {
         const _Float16* const stage = lds[s % kStages];
-        const int pos = ((quarter * 2 + (lane >> 5)) ^ ((lane >> 1) & 7)) * 8;
-        if (k < TI)
-            fp[into][k] = *reinterpret_cast<const half8*>(stage + (row_p + k * 32) * 64 + pos);
+        const int lo = k / (TI + TJ), f = k % (TI + TJ);
+        const int pos = ((lo * 4 + part * 2 + (lane >> 5)) ^ ((lane >> 1) & 7)) * 8;
+        if (f < TI)
+            fp[into][lo][f] = *reinterpret_cast<const half8*>(stage + (row_p + f * 32) * 64 + pos);
         else
-            fq[into][k - TI] = *reinterpret_cast<const half8*>(stage + (row_q + (k - TI) * 32) * 64 + pos);
+            fq[into][lo][f - TI] = *reinterpret_cast<const half8*>(stage + (row_q + (f - TI) * 32) * 64 + pos);
     };
     float16v acc[TJ][TI];
 #pragma unroll
@@ -450,22 +462,23 @@ __global__ __launch_bounds__(256, 1) void product_kernel(ProductArgs g) {
     auto multiply = [&](int with, int first, int last) {
 #pragma unroll
         for (int m = first; m < last; ++m) {
-            const int a = m / TJ, b = m % TJ;
-            acc[b][a] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fp[with][a], fq[with][b], acc[b][a], 0, 0, 0);
+            const int a = m % (TI * TJ) / TJ, b = m % TJ, term = m / (TI * TJ);  // hi hi, hi lo, lo hi
+            acc[b][a] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fp[with][term == 2][a], fq[with][term == 1][b], acc[b][a], 0, 0, 0);
         }
     };
-    // A stage's loads go out as soon as it is free, in the last quarter of the
+    // A stage's loads go out as soon as it is free, in the last part of the
     // step that used it; large tiles leave half of them to the next step's
-    // first two quarters, as one burst would hold up the products (8192 x
+    // first parts, as one burst would hold up the products (8192 x
     // 8192: 11.4 ms against 11.7).
     constexpr bool kSpread = TI * TJ >= 8;
     constexpr int kFirst = kSpread ? kLoads / 2 : kLoads, kSecond = kSpread ? kLoads * 3 / 4 : kLoads;
+    static_assert(!(kSpread && PAIRED), "two parts leave no third for the last loads");
     constexpr int kEarly = kSpread ? 4 : 0;  // products that cover the barrier
     // MAIN: the step s + 2 exists.
     auto step = [&](int s, auto main) {
         constexpr bool kMain = main.value;
 #pragma unroll
-        for (int sub = 0; sub < 3; ++sub) {
+        for (int sub = 0; sub < kParts - 1; ++sub) {
 #pragma unroll
             for (int k = 0; k < kReads; ++k) {
                 multiply(sub & 1, k * kMul / kReads, (k + 1) * kMul / kReads);
@@ -622,27 +635,44 @@ Plan plan_of(int64_t rows, int64_t cols, int64_t count, bool split, bool update)
     const int64_t pieces = (rows * cols + 2047) / 2048, most = round_up(kSumBlocks / count, 64);
     p.sum_blocks = (int)(pieces < most ? pieces : most);
     p.part = p.sums + round_up(count * p.sum_blocks * 8, 256);
-    const int64_t sym = tiles(64 * p.tile), third = split ? 3 : 1;
-    p.gram_slices = slices_of(sym, third * p.n / 64, p.tile);
-    p.poly_slices = slices_of(sym, third * p.m / 64, p.tile);
+    const int64_t sym = tiles(64 * p.tile);
+    p.gram_slices = slices_of(sym, (split ? 3 : 1) * p.n / 64, p.tile);
+    p.poly_slices = slices_of(sym, (split ? 2 : 1) * p.m / 64, p.tile);
     const int64_t slices = p.gram_slices > p.poly_slices ? p.gram_slices : p.poly_slices;
     // The sums of squares lie behind what either way needs.
     p.total = p.part + (slices > 1 ? sym * slices * p.tile * p.tile * 4 * 256 * 16 : 0);
     return p;
 }
 
-template <int T, bool SPLIT, int KIND>
+// The last product's output: the lanes' four consecutive elements run along i,
+// out's columns.
+void set_output(const UpdateArgs& u, ProductArgs* g) {
+    g->out = u.out;
+    g->out_i = u.cols;
+    g->out_j = u.rows;
+    g->out_aligned = aligned4(u.out);
+    g->update = u.momentum != nullptr;
+    g->keep = u.keep;
+    g->move = u.move;
+}
+
+template <int T, int TERMS, int KIND>
 void run_symmetric(ProductArgs g, int slices, int64_t count, hipStream_t stream) {
     const unsigned tiles = (unsigned)(count * g.tiles_i * (g.tiles_i + 1) / 2);
     g.slices = slices;
-    product_kernel<T, T, SPLIT, KIND><<<tiles * slices, 256, 0, stream>>>(g);
+    product_kernel<T, T, TERMS, KIND><<<tiles * slices, 256, 0, stream>>>(g);
     if constexpr (T < 4)  // where the largest tiles are taken there are enough of them
-        if (slices > 1) join_kernel<T, SPLIT, KIND><<<tiles * 4 * T, 64, 0, stream>>>(g);
+        if (slices > 1) join_kernel<T, TERMS != kPlain, KIND><<<tiles * 4 * T, 64, 0, stream>>>(g);
 }
 
 template <int T, bool SPLIT>
 hipError_t run_products(const UpdateArgs& u, const Plan& p, char* ws, hipStream_t stream) {
     constexpr int B = 64 * T;
+    // Split operands hold the diagonals well enough: they stay in the matrices,
+    // with a I in B's, and the step needs no old X.
+    constexpr int kGramTerms = SPLIT ? kInTurn : kPlain, kTerms = !SPLIT ? kPlain : T < 4 ? kPaired : kInTurn;
+    constexpr int kGramKind = SPLIT ? kSym : kGram, kPolyKind = SPLIT ? kSym : kPoly;
+    constexpr int kStepKind = SPLIT ? kFull : kStep, kLastKind = SPLIT ? kEnd : kLast;
     const bool tall = u.rows > u.cols;
     const int tm = (int)(p.m / B), tn = (int)(p.n / B);
     auto at = [&](int64_t o) { return reinterpret_cast<_Float16*>(ws + o); };
@@ -658,21 +688,28 @@ hipError_t run_products(const UpdateArgs& u, const Plan& p, char* ws, hipStream_
         g.p = g.q = at(p.x);
         g.ldp = g.ldq = p.n;
         g.k_steps = (int)(p.n / 64);
+        g.old = nullptr;
         g.c = g.ct = at(p.a);
         g.ldc = g.ldct = p.m;
         g.diag_in = nullptr;
         g.diag_out = reinterpret_cast<float*>(ws + p.da);
-        run_symmetric<T, SPLIT, kGram>(g, p.gram_slices, u.count, stream);
+        g.alpha = kScaleA / (kScaleX * kScaleX), g.beta = g.gamma = 0;
+        run_symmetric<T, kGramTerms, kGramKind>(g, p.gram_slices, u.count, stream);
         g.p = g.q = g.old = at(p.a);
         g.ldp = g.ldq = g.ldold = p.m;
         g.k_steps = (int)(p.m / 64);
         g.c = g.ct = at(p.b);
         g.diag_in = reinterpret_cast<const float*>(ws + p.da);
         g.diag_out = reinterpret_cast<float*>(ws + p.db);
-        run_symmetric<T, SPLIT, kPoly>(g, p.poly_slices, u.count, stream);
+        // a I + B times a power of two that keeps it within fp16's range
+        float p_scale = 16384.0f;
+        for (float f = 1; f < u.factors[s]; f *= 2) p_scale *= 0.5f;
+        g.alpha = g.k.c * p_scale / (kScaleA * kScaleA), g.beta = g.k.b * p_scale / kScaleA, g.gamma = g.k.a * p_scale;
+        run_symmetric<T, kTerms, kPolyKind>(g, p.poly_slices, u.count, stream);
         g.diag_in = reinterpret_cast<const float*>(ws + p.db);
         g.diag_out = nullptr;
         g.slices = 1;
+        g.alpha = 1 / p_scale;
         if (s + 1 < u.n_steps) {
             g.tiles_j = tn;
             g.p = at(p.b);
@@ -680,19 +717,13 @@ hipError_t run_products(const UpdateArgs& u, const Plan& p, char* ws, hipStream_
             g.c = at(p.x);
             g.ldc = p.n;
             g.ct = at(xt_next);
-            product_kernel<T, T, SPLIT, kStep><<<full, 256, 0, stream>>>(g);
+            product_kernel<T, T, kTerms, kStepKind><<<full, 256, 0, stream>>>(g);
             const int64_t was = xt;
             xt = xt_next;
             xt_next = was;
         } else {
-            // The lanes' four consecutive elements run along i: out's columns.
-            g.out = u.out;
-            g.out_i = u.cols;
-            g.out_j = u.rows;
-            g.out_aligned = aligned4(u.out);
-            g.update = u.momentum != nullptr;
-            g.keep = u.keep;
-            g.move = u.move;
+            set_output(u, &g);
+            g.alpha /= kScaleX;
             g.diag_by_i = tall;
             g.p = at(tall ? p.b : xt);
             g.q = at(tall ? xt : p.b);
@@ -700,7 +731,7 @@ hipError_t run_products(const UpdateArgs& u, const Plan& p, char* ws, hipStream_
             g.ldold = tall ? p.m : p.n;
             g.tiles_i = tall ? tm : tn;
             g.tiles_j = tall ? tn : tm;
-            product_kernel<T, T, SPLIT, kLast><<<full, 256, 0, stream>>>(g);
+            product_kernel<T, T, kTerms, kLastKind><<<full, 256, 0, stream>>>(g);
         }
     }
     return hipGetLastError();
@@ -740,7 +771,7 @@ hipError_t run_by_gram(const UpdateArgs& u, const Plan& p, char* ws, hipStream_t
         g.old = old < 0 ? nullptr : at(old);
         g.c = g.ct = at(to);
         g.alpha = alpha, g.beta = beta, g.gamma = gamma;
-        product_kernel<4, 4, true, kSym><<<sym, 256, 0, stream>>>(g);
+        product_kernel<4, 4, kInTurn, kSym><<<sym, 256, 0, stream>>>(g);
     };
     const int64_t r = p.a, t = p.b;
     int64_t xt = p.xt0, xt_next = p.xt1;
@@ -756,7 +787,7 @@ hipError_t run_by_gram(const UpdateArgs& u, const Plan& p, char* ws, hipStream_t
         g.old = nullptr;
         g.c = g.ct = at(r);
         g.alpha = kScaleR / (kScaleX * kScaleX), g.beta = g.gamma = 0;
-        product_kernel<4, 4, true, kSym><<<sym, 256, 0, stream>>>(g);
+        product_kernel<4, 4, kInTurn, kSym><<<sym, 256, 0, stream>>>(g);
         int64_t poly = p.c[0], q = p.c[1], q_next = p.c[2];
         for (int s = from; s < to; ++s) {
             const Quintic& k = u.steps[s];
@@ -785,24 +816,18 @@ hipError_t run_by_gram(const UpdateArgs& u, const Plan& p, char* ws, hipStream_t
             g.c = at(p.x), g.ldc = p.n;
             g.ct = at(xt_next), g.ldct = p.m;
             g.alpha = 1 / scale;
-            product_kernel<4, 4, true, kFull><<<full, 256, 0, stream>>>(g);
+            product_kernel<4, 4, kInTurn, kFull><<<full, 256, 0, stream>>>(g);
             const int64_t was = xt;
             xt = xt_next;
             xt_next = was;
         } else {
-            g.out = u.out;
-            g.out_i = u.cols;
-            g.out_j = u.rows;
-            g.out_aligned = aligned4(u.out);
-            g.update = u.momentum != nullptr;
-            g.keep = u.keep;
-            g.move = u.move;
+            set_output(u, &g);
             g.alpha = 1 / (scale * kScaleX);
             g.p = at(tall ? q : xt);
             g.q = at(tall ? xt : q);
             g.tiles_i = tall ? tm : tn;
             g.tiles_j = tall ? tn : tm;
-            product_kernel<4, 4, true, kEnd><<<full, 256, 0, stream>>>(g);
+            product_kernel<4, 4, kInTurn, kEnd><<<full, 256, 0, stream>>>(g);
         }
     }
     return hipGetLastError();
