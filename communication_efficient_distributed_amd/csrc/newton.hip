@@ -29,6 +29,7 @@ namespace sl {
 namespace {
 
 constexpr float kScaleX = 8192.0f, kScaleA = 4096.0f, kScaleB = 2048.0f;
+constexpr int kUnits = 256;       // compute units
 constexpr int kSumBlocks = 1024;  // of all matrices' partial sums of squares, about
 
 // ---------------------------------------------------------------------------
@@ -152,7 +153,8 @@ struct ProductArgs {
     int64_t matrix_bytes;    // from one matrix's arrays to the next one's
     int32_t k_steps;         // summed index / 64
     int32_t tiles_i, tiles_j;
-    int32_t slices;          // of the summed index; with more than one, sums go to `part`
+    int32_t whole;           // tiles done by one block each, before those that are sliced
+    int32_t slices;          // of the summed index for the others, whose sums go to `part`
     float4* part;
     // epilogue
     const _Float16* old;     // poly: A; step, last: X, so that old[j * ldold + i] meets C[i][j]
@@ -403,8 +405,12 @@ __global__ __launch_bounds__(256, 1) void product_kernel(ProductArgs g) {
     const int lane = lane_id(), wave = uniform(threadIdx.x >> 6);
     const int wi = wave >> 1, wj = wave & 1;
     const int tiles = symmetric(KIND) ? g.tiles_i * (g.tiles_i + 1) / 2 : g.tiles_i * g.tiles_j;
-    const int block = xcd_order(blockIdx.x, gridDim.x);
-    const int slice = block % g.slices, t = block / g.slices;
+    // Symmetric products: tiles by one block each first, then the sliced ones.
+    const int whole = symmetric(KIND) ? g.whole : gridDim.x;
+    const bool sliced = symmetric(KIND) && (int)blockIdx.x >= whole;
+    const int slices = sliced ? g.slices : 1;
+    const int block = sliced ? xcd_order(blockIdx.x - whole, gridDim.x - whole) : xcd_order(blockIdx.x, whole);
+    const int slice = block % slices, t = (sliced ? whole : 0) + block / slices;
     const int64_t matrix = t / tiles;
     int ti, tj;
     if (symmetric(KIND))
@@ -413,7 +419,7 @@ __global__ __launch_bounds__(256, 1) void product_kernel(ProductArgs g) {
         full_tile(t % tiles, g.tiles_i, g.tiles_j, &ti, &tj);
     const int64_t shift = matrix * (g.matrix_bytes / 2);
     const int all = g.k_steps * (PAIRED ? 2 : SPLIT ? 3 : 1);
-    const int from = all * slice / g.slices, steps = all * (slice + 1) / g.slices - from;
+    const int from = all * slice / slices, steps = all * (slice + 1) / slices - from;
 
     // Loads: a wavefront instruction fills 8 rows of 64 elements.  The 16-byte
     // piece c of row r sits at position c ^ (r / 2 & 7), so that the 16 lanes
@@ -519,8 +525,8 @@ __global__ __launch_bounds__(256, 1) void product_kernel(ProductArgs g) {
     for (; s + 2 < steps; ++s) step(s, Constant<1>{});
     for (; s < steps; ++s) step(s, Constant<0>{});
 
-    if (TI < 4 && symmetric(KIND) && g.slices > 1) {
-        float4* part = g.part + ((int64_t)t * g.slices + slice) * (TI * TJ * 4 * 256) + threadIdx.x;
+    if (sliced) {
+        float4* part = g.part + ((int64_t)(t - whole) * slices + slice) * (TI * TJ * 4 * 256) + threadIdx.x;
 #pragma unroll
         for (int b = 0; b < TJ; ++b)
 #pragma unroll
@@ -545,10 +551,10 @@ template <int T, bool SPLIT, int KIND>
 __global__ __launch_bounds__(64) void join_kernel(ProductArgs g) {
     __shared__ __attribute__((aligned(16))) float strip[32 * strip_pitch(T)];
     const int tiles = g.tiles_i * (g.tiles_i + 1) / 2;
-    const int b = blockIdx.x % T, wave = blockIdx.x / T % 4, t = blockIdx.x / (4 * T);
+    const int b = blockIdx.x % T, wave = blockIdx.x / T % 4, sliced = blockIdx.x / (4 * T), t = g.whole + sliced;
     int ti, tj;
     symmetric_tile(t % tiles, g.tiles_i, &ti, &tj);
-    const float4* part = g.part + (int64_t)t * g.slices * (T * T * 4 * 256) + b * T * 4 * 256 + wave * 64 + lane_id();
+    const float4* part = g.part + (int64_t)sliced * g.slices * (T * T * 4 * 256) + b * T * 4 * 256 + wave * 64 + lane_id();
     float16v acc[T];
 #pragma unroll
     for (int a = 0; a < T; ++a) acc[a] = 0.0f;
@@ -579,6 +585,7 @@ struct Plan {
     int64_t sums, part;    // byte offsets of the partial sums of squares and of sliced products
     int64_t total;
     int sum_blocks;
+    int64_t whole;         // tiles of a symmetric product that are not sliced
     int gram_slices, poly_slices;
 };
 
@@ -589,11 +596,20 @@ bool aligned4(const MatrixView& v) {
 
 int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
-// Slices of a symmetric product of `tiles` tiles and `steps` steps: enough
-// blocks to fill the chip, none shorter than 6 steps.
+// How many of `tiles` tiles of a symmetric product get a block each, the rest
+// being sliced.  Small tiles: all or none.  256 x 256 tiles, one of which a
+// compute unit holds: as many as fill the chip a whole number of times, if the
+// rest would leave most of it idle (8192 x 8192: 512 of 528).
+int64_t whole_of(int64_t tiles, int tile) {
+    if (tile < 4) return 2 * tiles > (tile == 2 ? 512 : 1024) ? tiles : 0;
+    return tiles % kUnits <= kUnits / 4 ? tiles - tiles % kUnits : tiles;
+}
+
+// Slices of each of `tiles` tiles that take `steps` steps: enough blocks to
+// fill the chip, none shorter than 6 steps.
 int slices_of(int64_t tiles, int64_t steps, int tile) {
-    if (tile == 4) return 1;
-    const int64_t room = tile == 2 ? 512 : 1024;  // blocks that run at once
+    if (tiles == 0) return 1;
+    const int64_t room = tile == 4 ? kUnits : tile == 2 ? 512 : 1024;  // blocks that run at once
     const int64_t want = room / tiles, most = steps / 6;
     return (int)(want < 2 || most < 2 ? 1 : want < most ? want : most);
 }
@@ -635,12 +651,13 @@ Plan plan_of(int64_t rows, int64_t cols, int64_t count, bool split, bool update)
     const int64_t pieces = (rows * cols + 2047) / 2048, most = round_up(kSumBlocks / count, 64);
     p.sum_blocks = (int)(pieces < most ? pieces : most);
     p.part = p.sums + round_up(count * p.sum_blocks * 8, 256);
-    const int64_t sym = tiles(64 * p.tile);
-    p.gram_slices = slices_of(sym, (split ? 3 : 1) * p.n / 64, p.tile);
-    p.poly_slices = slices_of(sym, (split ? 2 : 1) * p.m / 64, p.tile);
+    const int64_t sym = tiles(64 * p.tile), per_step = split ? p.tile < 4 ? 2 : 3 : 1;
+    p.whole = whole_of(sym, p.tile);
+    p.gram_slices = slices_of(sym - p.whole, (split ? 3 : 1) * p.n / 64, p.tile);
+    p.poly_slices = slices_of(sym - p.whole, per_step * p.m / 64, p.tile);
     const int64_t slices = p.gram_slices > p.poly_slices ? p.gram_slices : p.poly_slices;
     // The sums of squares lie behind what either way needs.
-    p.total = p.part + (slices > 1 ? sym * slices * p.tile * p.tile * 4 * 256 * 16 : 0);
+    p.total = p.part + (slices > 1 ? (sym - p.whole) * slices * p.tile * p.tile * 4 * 256 * 16 : 0);
     return p;
 }
 
@@ -656,13 +673,15 @@ void set_output(const UpdateArgs& u, ProductArgs* g) {
     g->move = u.move;
 }
 
+// A symmetric product, of whose tiles those after the first `whole` are sliced.
 template <int T, int TERMS, int KIND>
-void run_symmetric(ProductArgs g, int slices, int64_t count, hipStream_t stream) {
-    const unsigned tiles = (unsigned)(count * g.tiles_i * (g.tiles_i + 1) / 2);
+void run_symmetric(ProductArgs g, int64_t whole, int slices, int64_t count, hipStream_t stream) {
+    const int64_t tiles = count * g.tiles_i * (g.tiles_i + 1) / 2;
+    g.whole = (int32_t)(slices > 1 ? whole : tiles);
     g.slices = slices;
-    product_kernel<T, T, TERMS, KIND><<<tiles * slices, 256, 0, stream>>>(g);
-    if constexpr (T < 4)  // where the largest tiles are taken there are enough of them
-        if (slices > 1) join_kernel<T, TERMS != kPlain, KIND><<<tiles * 4 * T, 64, 0, stream>>>(g);
+    const int64_t rest = tiles - g.whole;
+    product_kernel<T, T, TERMS, KIND><<<(unsigned)(g.whole + rest * slices), 256, 0, stream>>>(g);
+    if (rest) join_kernel<T, TERMS != kPlain, KIND><<<(unsigned)(rest * 4 * T), 64, 0, stream>>>(g);
 }
 
 template <int T, bool SPLIT>
@@ -694,7 +713,7 @@ hipError_t run_products(const UpdateArgs& u, const Plan& p, char* ws, hipStream_
         g.diag_in = nullptr;
         g.diag_out = reinterpret_cast<float*>(ws + p.da);
         g.alpha = kScaleA / (kScaleX * kScaleX), g.beta = g.gamma = 0;
-        run_symmetric<T, kGramTerms, kGramKind>(g, p.gram_slices, u.count, stream);
+        run_symmetric<T, kGramTerms, kGramKind>(g, p.whole, p.gram_slices, u.count, stream);
         g.p = g.q = g.old = at(p.a);
         g.ldp = g.ldq = g.ldold = p.m;
         g.k_steps = (int)(p.m / 64);
@@ -705,10 +724,9 @@ hipError_t run_products(const UpdateArgs& u, const Plan& p, char* ws, hipStream_
         float p_scale = 16384.0f;
         for (float f = 1; f < u.factors[s]; f *= 2) p_scale *= 0.5f;
         g.alpha = g.k.c * p_scale / (kScaleA * kScaleA), g.beta = g.k.b * p_scale / kScaleA, g.gamma = g.k.a * p_scale;
-        run_symmetric<T, kTerms, kPolyKind>(g, p.poly_slices, u.count, stream);
+        run_symmetric<T, kTerms, kPolyKind>(g, p.whole, p.poly_slices, u.count, stream);
         g.diag_in = reinterpret_cast<const float*>(ws + p.db);
         g.diag_out = nullptr;
-        g.slices = 1;
         g.alpha = 1 / p_scale;
         if (s + 1 < u.n_steps) {
             g.tiles_j = tn;
@@ -760,8 +778,8 @@ hipError_t run_by_gram(const UpdateArgs& u, const Plan& p, char* ws, hipStream_t
     ProductArgs g = {};
     g.lo = p.lo;
     g.matrix_bytes = p.matrix_bytes;
-    g.slices = 1;
-    const unsigned sym = (unsigned)(u.count * (tm * (tm + 1) / 2)), full = (unsigned)(u.count * tm * tn);
+    g.part = reinterpret_cast<float4*>(ws + p.part);
+    const unsigned full = (unsigned)(u.count * tm * tn);
     // to = alpha a b + beta old + gamma I, all m x m.
     auto square = [&](int64_t to, int64_t a, int64_t b, float alpha, int64_t old, float beta, float gamma) {
         g.tiles_i = g.tiles_j = tm;
@@ -771,7 +789,7 @@ hipError_t run_by_gram(const UpdateArgs& u, const Plan& p, char* ws, hipStream_t
         g.old = old < 0 ? nullptr : at(old);
         g.c = g.ct = at(to);
         g.alpha = alpha, g.beta = beta, g.gamma = gamma;
-        product_kernel<4, 4, kInTurn, kSym><<<sym, 256, 0, stream>>>(g);
+        run_symmetric<4, kInTurn, kSym>(g, p.whole, p.poly_slices, u.count, stream);
     };
     const int64_t r = p.a, t = p.b;
     int64_t xt = p.xt0, xt_next = p.xt1;
@@ -787,7 +805,7 @@ hipError_t run_by_gram(const UpdateArgs& u, const Plan& p, char* ws, hipStream_t
         g.old = nullptr;
         g.c = g.ct = at(r);
         g.alpha = kScaleR / (kScaleX * kScaleX), g.beta = g.gamma = 0;
-        product_kernel<4, 4, kInTurn, kSym><<<sym, 256, 0, stream>>>(g);
+        run_symmetric<4, kInTurn, kSym>(g, p.whole, p.gram_slices, u.count, stream);
         int64_t poly = p.c[0], q = p.c[1], q_next = p.c[2];
         for (int s = from; s < to; ++s) {
             const Quintic& k = u.steps[s];
