@@ -619,10 +619,13 @@ Plan plan_of(int64_t rows, int64_t cols, int64_t count, bool split, bool update)
     const int64_t m = rows < cols ? rows : cols, n = rows < cols ? cols : rows;
     auto tiles = [&](int64_t t) { const int64_t k = (m + t - 1) / t; return count * k * (k + 1) / 2; };
     // Larger tiles do more products for each byte they read, smaller ones fill
-    // the chip with less work.  Measured in all (256 / 128 / 64): 4096 x 4096
-    // 1.85 / 1.95 / 2.42 ms; 8 x 1024 x 1024 625 / 420 / 442 us; 2048 x 2048
-    // 681 / 451 / 420 us, split 1250 / 841 / 982 us.
-    p.tile = tiles(256) >= 128 ? 4 : tiles(128) >= (split ? 36 : 160) ? 2 : 1;
+    // the chip with less work and pad less.  Measured in all (256 / 128 / 64),
+    // us: 4096 x 4096 1.85 / 1.95 / 2.42 ms, 3000 x 3000 1226 / 955 / 1118,
+    // 2500 x 2500 811 / 598 / 692, 2048 x 2048 664 / 418 / 387, 16 of 700 x 900
+    // 708 / 431 / 388; split 5000 x 5000 7.3 / 9.0 / 13.7 ms, 1024 x 8192 797 /
+    // 638 / 782, 1000 x 1500 two of 708 / 407 / 418, 1024 x 1024 630 / 330 / 262.
+    const double products = (double)count * m * m * n;
+    p.tile = tiles(256) >= 128 ? 4 : products >= (split ? 2.5e9 : 1e10) ? 2 : 1;
     p.m = round_up(m, 64 * p.tile);
     p.n = round_up(n, 64 * p.tile);
     // All hi arrays, then all lo arrays in the same order.
