@@ -49,11 +49,16 @@ def _buffer(t: torch.Tensor | None, name: str, dtype, shape, device) -> int | No
     return t.data_ptr()
 
 
+# The current stream's handle without a Stream object around it, where torch has it.
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _call(name: str, device, args, stream) -> None:
     """Calls the library with the device current and the stream last; torch's
     device guard only where another device is current, since it costs as much
     as a kernel launch."""
-    handle = torch.cuda.current_stream(device).cuda_stream if stream is None else \
+    handle = _current_stream(device.index) if stream is None else \
         int(stream.cuda_stream if hasattr(stream, "cuda_stream") else stream)
     fn = getattr(load(), name)
     if torch.cuda.current_device() == device.index:
@@ -139,7 +144,7 @@ def sl_orthogonalize(x: torch.Tensor, out: torch.Tensor, coefficients=SL_NEWTON_
     """out = the Newton-Schulz orthogonalisation of x ([rows, cols] or [count,
     rows, cols], float32, bfloat16 or float16, adjacent columns; rows and
     matrices may be strided).  products: 'f16' (within about 1e-3 of the exact
-    result) or 'split' (about 2e-6, three times the products); by default
+    result) or 'split' (about 3e-6, three times the products); by default
     'split' for a float32 out and 'f16' for a 16-bit one.  workspace: a buffer
     of orthogonalize_workspace() bytes to use again; by default one from torch's
     allocator."""
@@ -169,7 +174,8 @@ def sl_muon_step(theta: torch.Tensor, momentum: torch.Tensor, grad: torch.Tensor
     theta <- theta * (1 - lr * weight_decay) - lr * update_scale *
     orthogonalize(u).  As an outer update, grad is the sum of sl_aggregate and
     grad_scale 1 / n_peers.  products and workspace as for sl_orthogonalize
-    (default by theta's type)."""
+    (default by theta's type; 'split' is within about 1e-5 for large matrices
+    that are not square), the latter of muon_step_workspace() bytes."""
     _gpu(theta, "theta", (torch.float32, torch.bfloat16)), _gpu(grad, "grad", (torch.float32, torch.bfloat16))
     if theta.dim() not in (2, 3):
         raise ValueError("theta must be [rows, cols] or [count, rows, cols]")

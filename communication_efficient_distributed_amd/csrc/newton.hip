@@ -651,7 +651,7 @@ Plan plan_of(int64_t rows, int64_t cols, int64_t count, bool split, bool update)
     p.sums = count * at > narrow ? count * at : narrow;
     // A few pieces of 2048 elements for each block of the sums of squares, and
     // few enough blocks that the next kernel adds them up in no time.
-    const int64_t pieces = (rows * cols + 2047) / 2048, most = round_up(kSumBlocks / count, 64);
+    const int64_t pieces = (rows * cols + 2047) / 2048, most = round_up(kSumBlocks / count + 1, 64);
     p.sum_blocks = (int)(pieces < most ? pieces : most);
     p.part = p.sums + round_up(count * p.sum_blocks * 8, 256);
     const int64_t sym = tiles(64 * p.tile), per_step = split ? p.tile < 4 ? 2 : 3 : 1;

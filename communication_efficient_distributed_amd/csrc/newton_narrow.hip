@@ -209,27 +209,34 @@ __global__ __launch_bounds__(BLOCKS*(BLOCKS + 1) / 2 * kWave) void narrow_steps_
     int ti, tj;
     triangle_tile(t, &ti, &tj);
     const int j = lane & 31, i4 = 4 * (lane >> 5);
-
-    // This wavefront's tile, and its mirror image, to a pair in LDS.
-    auto put = [&](_Float16* to, const float16v& v, float scale) {
+    // Where the tile's rows of four go in a pair, and the elements of its mirror image.
+    int direct[4], mirror[16];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+        mirror[r] = cell(ti * 32 + (r >> 2) * 8 + i4 + (r & 3), tj * 32 + j);
+        if ((r & 3) == 0) direct[r >> 2] = cell(tj * 32 + j, ti * 32 + (r >> 2) * 8 + i4);
+    }
+    const bool turned = ti != tj;
+    // To a pair in LDS: hi is cut off towards zero, lo the rest (2^-21 of the
+    // value at most stays behind), which takes half the instructions that two
+    // rounded conversions would; those, not the products, bound the kernel.
+    auto put = [&](_Float16* to, const float16v& v) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            half4 h, l;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                _Float16 hh, ll;
-                split_half(v[r * 4 + e] * scale, &hh, &ll);
-                h[e] = hh;
-                l[e] = ll;
-                if (ti != tj) {
-                    const int at = cell(ti * 32 + r * 8 + i4 + e, tj * 32 + j);
-                    to[at] = hh;
-                    to[at + kSide * kSide] = ll;
-                }
+            const half2 h0 = __builtin_bit_cast(half2, __builtin_amdgcn_cvt_pkrtz(v[r * 4], v[r * 4 + 1]));
+            const half2 h1 = __builtin_bit_cast(half2, __builtin_amdgcn_cvt_pkrtz(v[r * 4 + 2], v[r * 4 + 3]));
+            const half2 l0 = __builtin_bit_cast(
+                half2, __builtin_amdgcn_cvt_pkrtz(__builtin_fmaf((float)h0[0], -1.0f, v[r * 4]), __builtin_fmaf((float)h0[1], -1.0f, v[r * 4 + 1])));
+            const half2 l1 = __builtin_bit_cast(
+                half2, __builtin_amdgcn_cvt_pkrtz(__builtin_fmaf((float)h1[0], -1.0f, v[r * 4 + 2]), __builtin_fmaf((float)h1[1], -1.0f, v[r * 4 + 3])));
+            *reinterpret_cast<half4*>(to + direct[r]) = half4{h0[0], h0[1], h1[0], h1[1]};
+            *reinterpret_cast<half4*>(to + direct[r] + kSide * kSide) = half4{l0[0], l0[1], l1[0], l1[1]};
+            if (turned) {
+                to[mirror[r * 4]] = h0[0], to[mirror[r * 4] + kSide * kSide] = l0[0];
+                to[mirror[r * 4 + 1]] = h0[1], to[mirror[r * 4 + 1] + kSide * kSide] = l0[1];
+                to[mirror[r * 4 + 2]] = h1[0], to[mirror[r * 4 + 2] + kSide * kSide] = l1[0];
+                to[mirror[r * 4 + 3]] = h1[1], to[mirror[r * 4 + 3] + kSide * kSide] = l1[1];
             }
-            const int at = cell(tj * 32 + j, ti * 32 + r * 8 + i4);
-            *reinterpret_cast<half4*>(to + at) = h;
-            *reinterpret_cast<half4*>(to + at + kSide * kSide) = l;
         }
     };
     // The product of two symmetric pairs that commute: symmetric too.
@@ -250,6 +257,8 @@ __global__ __launch_bounds__(BLOCKS*(BLOCKS + 1) / 2 * kWave) void narrow_steps_
         return sum;
     };
 
+    // R times kScaleR, P times kScaleP, Q times scale_q: powers of two, so that
+    // registers and LDS hold the same values.
     float16v rr, q;
 #pragma unroll
     for (int r = 0; r < 16; ++r) rr[r] = q[r] = 0;
@@ -261,42 +270,47 @@ __global__ __launch_bounds__(BLOCKS*(BLOCKS + 1) / 2 * kWave) void narrow_steps_
             rr[r * 4] += v.x, rr[r * 4 + 1] += v.y, rr[r * 4 + 2] += v.z, rr[r * 4 + 3] += v.w;
         }
 #pragma unroll
-    for (int r = 0; r < 16; ++r) rr[r] *= 1.0f / (kScaleX * kScaleX);
-    put(first, rr, kScaleR);
+    for (int r = 0; r < 16; ++r) rr[r] *= kScaleR / (kScaleX * kScaleX);
+    put(first, rr);
     for (int k = 0; k < steps.n; ++k) {
         const Quintic z = steps.k[k];
         __syncthreads();
-        float16v p = product(first, first, z.c / (kScaleR * kScaleR));
+        float16v p = product(first, first, z.c * (kScaleP / (kScaleR * kScaleR)));
+        const float zb = z.b * (kScaleP / kScaleR);
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            p[r] = __builtin_fmaf(z.b, rr[r], p[r]);
-            if (ti == tj && j == (r >> 2) * 8 + i4 + (r & 3)) p[r] += z.a;
+        for (int r = 0; r < 16; ++r) p[r] = __builtin_fmaf(zb, rr[r], p[r]);
+        if (!turned) {
+            const float za = z.a * kScaleP;
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                if (j == (r >> 2) * 8 + i4 + (r & 3)) p[r] += za;
         }
-        put(second, p, kScaleP);
+        put(second, p);
         const bool last = k + 1 == steps.n;
         if (!last) {  // R <- (P R) P
             __syncthreads();
-            const float16v pr = product(second, first, 1.0f / (kScaleP * kScaleR));
+            const float16v pr = product(second, first, 1.0f / kScaleP);
             __syncthreads();
-            put(first, pr, kScaleR);
+            put(first, pr);
             __syncthreads();
-            rr = product(first, second, 1.0f / (kScaleP * kScaleR));
+            rr = product(first, second, 1.0f / kScaleP);
         }
         if (k == 0) {
-            q = p;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) q[r] = p[r] * (scale_q / kScaleP);
         } else {  // Q <- Q P
             __syncthreads();
-            put(first, q, scale_q);
+            put(first, q);
             __syncthreads();
-            q = product(first, second, 1.0f / (kScaleP * scale_q));
+            q = product(first, second, 1.0f / kScaleP);
         }
         if (!last) {
             __syncthreads();
-            put(first, rr, kScaleR);
+            put(first, rr);
         }
     }
     __syncthreads();
-    put(first, q, scale_q);
+    put(first, q);
     __syncthreads();
     // Straight rows to memory; what lies beyond m was never set and is zero here.
     _Float16* const out = q_out + (int64_t)blockIdx.x * 2 * kSide * kSide;
@@ -388,17 +402,21 @@ __global__ __launch_bounds__(256, 2) void narrow_apply_kernel(NarrowArgs a, int6
                     }
                     store_values4(o.out.ptr, o.out.type, at + col, v);
                 }
-        } else {
+        } else {  // element by element, the registers taking turns in one place
+#pragma unroll 1
+            for (int r = 0; r < 32; ++r) {
+                const float sum = acc[0][0];
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+                for (int e = 0; e < 15; ++e) acc[0][e] = acc[0][e + 1];
+                acc[0][15] = acc[1][0];
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int64_t col = col0 + b * 32 + (r >> 2) * 8 + (r & 3);
-                    if (col >= a.cols) continue;
-                    float v = acc[b][r] * o.scale;
-                    if (o.update) v = __builtin_fmaf(-o.move, v, load_value(o.out.ptr, o.out.type, at + col) * o.keep);
-                    store_value(o.out.ptr, o.out.type, at + col, v);
-                }
+                for (int e = 0; e < 15; ++e) acc[1][e] = acc[1][e + 1];
+                const int64_t col = col0 + (r >> 4) * 32 + (r >> 2 & 3) * 8 + (r & 3);
+                if (col >= a.cols) continue;
+                float v = sum * o.scale;
+                if (o.update) v = __builtin_fmaf(-o.move, v, load_value(o.out.ptr, o.out.type, at + col) * o.keep);
+                store_value(o.out.ptr, o.out.type, at + col, v);
+            }
         }
     }
 }

@@ -81,8 +81,9 @@ sl_status read_steps(const float* coefficients, int32_t n, sl::Quintic* steps, s
         if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return SL_ERR_INVALID_ARG;
         if (!(top <= 3.8) || !(largest_poly(b, c, top * top) <= 30)) return SL_ERR_INVALID_ARG;
         const double factor = largest_factor(a, b, c, top * top);
+        if (!(factor <= 1e4)) return SL_ERR_INVALID_ARG;
         product *= factor;
-        u->factors[k] = (float)std::min(factor, 1e30);
+        u->factors[k] = (float)factor;
         grown = std::max(grown, factor > 100 ? 1e30 : product);
         top = largest_value(a, b, c, top);
         steps[k] = {a, b, c};

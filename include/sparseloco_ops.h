@@ -38,7 +38,9 @@ typedef enum {
                              within about 1e-3 of the exact one (2-norm of the
                              difference over 2-norm), finer than bf16 holds */
     SL_PRODUCTS_SPLIT = 1 /* each operand the sum of two fp16 values (22 bits), three
-                             products: within about 2e-6, at three times the work */
+                             products: within about 3e-6, at three times the work
+                             (sl_muon_step on matrices of some thousand rows and
+                             columns that are not square: about 1e-5) */
 } sl_products;
 
 #define SL_MAX_STEPS 16
@@ -65,8 +67,9 @@ typedef enum {
  *                rows * cols * count and min(rows, cols)^2 * count at most 2^40
  * coefficients   HOST float[n_steps][3].  Refused (SL_ERR_INVALID_ARG) if not
  *                finite, or if with singular values in [0, 1] to start from some
- *                iterate's would pass 3.8 or some b s^2 + c s^4 would pass 30 in
- *                magnitude: beyond that the fp16 operands could overflow
+ *                iterate's (the last step's result apart) would pass 3.8, some
+ *                b s^2 + c s^4 30 or some a + b s^2 + c s^4 10^4 in magnitude:
+ *                beyond that the fp16 operands could overflow
  * n_steps        1..SL_MAX_STEPS
  * eps            finite, >= 0
  * products       an sl_products

@@ -62,6 +62,17 @@ def test_large_vocabulary_many_rows():
         compare(run(sl, x, t, 20), logprobs(x, t, 20), x)
 
 
+def test_more_rows_than_a_grid_holds():
+    sl = require_gpu()
+    note("logprobs 70000 x 50")
+    g = torch.Generator().manual_seed(3)
+    x = (torch.randn(70000, 50, generator=g) * 3).bfloat16()
+    t = torch.randint(0, 50, (70000,), generator=g)
+    got = run(sl, x, t, 2)
+    some = torch.cat([torch.arange(40), torch.arange(65500, 65600), torch.arange(69960, 70000)])
+    compare([o.cpu()[some] for o in got], logprobs(x[some], t[some], 2), x)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
 def test_ties_go_to_the_lower_token(dtype):
     sl = require_gpu()

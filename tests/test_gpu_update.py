@@ -72,6 +72,18 @@ def test_orthogonalize_batches_and_larger_tiles(count, rows, cols, products):
         assert err <= tol, f"matrix {k}: {err:.3g} off, {tol:.3g} allowed"
 
 
+@pytest.mark.parametrize("products", ["f16", "split"])
+def test_orthogonalize_thousands_of_small_matrices(products):
+    sl = require_gpu()
+    note(f"orthogonalize 3000 of 20x24 {products}")
+    x = update_like((3000, 20, 24), 77)
+    out = torch.empty(x.shape, device="cuda")
+    sl.sl_orthogonalize(x.cuda(), out, products=products)
+    some = [0, 1, 1499, 2999]
+    check(out[some], x[some], products)
+    assert out.isfinite().all()
+
+
 def test_orthogonalize_strided_views_and_guards():
     """Rows and matrices of larger tensors, in and out; what lies between is left as it was."""
     sl = require_gpu()
