@@ -70,6 +70,18 @@ def _call(name: str, device, args, stream) -> None:
         _check(name, status)
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """New memory for a call on `stream` (None: the current one). It is that
+    stream's own: memory of the current one may still be in use by work queued
+    there, which `stream` does not wait for."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _strided(t: torch.Tensor, name: str):
     """(rows, cols, count, row stride, matrix stride) of a [rows, cols] or
     [count, rows, cols] tensor whose columns are adjacent."""
@@ -110,11 +122,7 @@ def _workspace(fn: str, need: int, workspace, device, stream):
     if workspace is None:
         if need == 0:
             return None, None, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        if stream is not None:
-            # torch may hand the memory out again on its own stream: tell it who uses it
-            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(
-                int(stream.cuda_stream if hasattr(stream, "cuda_stream") else stream), device=device))
+        workspace = _empty(need, torch.uint8, device, stream)
         return workspace, workspace.data_ptr(), need
     have = workspace.numel() * workspace.element_size()
     if have < need:
@@ -226,14 +234,15 @@ def sl_token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None, logpro
           (logits.data_ptr(), kind, ld, target, rows, vocab, n_top, *buffers, ws, ws_bytes), stream)
 
 
-# Convenience wrappers that allocate outputs with torch (device memory only).
+# Convenience wrappers that allocate outputs with torch (device memory only),
+# as memory of the stream they run on.
 
 def orthogonalize(x: torch.Tensor, out_dtype: torch.dtype | None = None, coefficients=SL_NEWTON_SCHULZ,
                   eps: float = 1e-7, products: str | None = None, workspace: torch.Tensor | None = None,
                   stream=None) -> torch.Tensor:
     """sl_orthogonalize into a new tensor of out_dtype (default x's type)."""
     _gpu(x, "x", _TYPES)
-    out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+    out = _empty(x.shape, out_dtype or x.dtype, x.device, stream)
     sl_orthogonalize(x, out, coefficients, eps, products, workspace, stream)
     return out
 
@@ -250,8 +259,8 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, n_top: int = 0, 
     top_index), the last two None for n_top = 0."""
     _gpu(logits, "logits", _TYPES)
     rows, dev = logits.shape[0], logits.device
-    logprob, entropy = torch.empty((2, rows), dtype=torch.float32, device=dev).unbind(0)
-    top_logprob = torch.empty((rows, n_top), dtype=torch.float32, device=dev) if n_top else None
-    top_index = torch.empty((rows, n_top), dtype=torch.int32, device=dev) if n_top else None
+    logprob, entropy = _empty((2, rows), torch.float32, dev, stream).unbind(0)
+    top_logprob = _empty((rows, n_top), torch.float32, dev, stream) if n_top else None
+    top_index = _empty((rows, n_top), torch.int32, dev, stream) if n_top else None
     sl_token_logprobs(logits, targets, logprob, entropy, top_logprob, top_index, workspace, stream)
     return logprob, entropy, top_logprob, top_index

@@ -173,6 +173,53 @@ def test_orthogonalize_repeats_bitwise_on_any_stream_and_workspace():
         assert torch.equal(first, o)
 
 
+def test_calls_on_another_stream_use_that_streams_memory():
+    """Memory that work queued on the current stream still reads is not taken for a call on another one."""
+    sl = require_gpu()
+    note("memory of another stream")
+    x = update_like((200, 300), 4).cuda()
+    logits, targets = torch.randn(64, 5000, device="cuda"), torch.arange(64, device="cuda")
+    other = torch.cuda.Stream()
+    calls = [(sl.orthogonalize_workspace(200, 300, 1, "split"), lambda: [sl.orthogonalize(x, stream=other)]),
+             (x.numel() * 4, lambda: [sl.orthogonalize(x, stream=other.cuda_stream)]),
+             (64 * 4 * 4, lambda: list(sl.token_logprobs(logits, targets, 4, stream=other)))]
+    for need, call in calls:
+        expected = call()
+        torch.cuda.synchronize()
+        kept, seen = torch.full((need,), 7, dtype=torch.uint8, device="cuda"), torch.zeros(need, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)           # some 10 ms before the copy
+        seen.copy_(kept)
+        del kept
+        got = call()
+        torch.cuda.synchronize()
+        assert (seen == 7).all()
+        for a, b in zip(expected, got):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("rows,cols,count,products", [(100, 700, 3, "f16"), (700, 100, 2, "f16"), (300, 4000, 1, "split"),
+                                                      (1100, 1300, 2, "split"), (4100, 4200, 1, "f16"),
+                                                      (4100, 6200, 1, "split")])
+def test_workspace_contents_do_not_matter(rows, cols, count, products):
+    """Every way through the products with a workspace of zeros and one of NaN patterns."""
+    sl = require_gpu()
+    note(f"workspace contents {count}x{rows}x{cols} {products}")
+    grad = torch.randn(count, rows, cols, generator=torch.Generator().manual_seed(9)).cuda()
+    results = []
+    for fill in (0, 255):
+        out = torch.empty_like(grad)
+        need = sl.orthogonalize_workspace(rows, cols, count, products)
+        sl.sl_orthogonalize(grad, out, products=products, workspace=torch.full((need,), fill, dtype=torch.uint8, device="cuda"))
+        theta, momentum = torch.ones_like(grad), torch.zeros_like(grad)
+        need = sl.muon_step_workspace(rows, cols, count, products)
+        sl.sl_muon_step(theta, momentum, grad, lr=0.1, products=products,
+                        workspace=torch.full((need,), fill, dtype=torch.uint8, device="cuda"))
+        results.append((out, theta, momentum))
+    for a, b in zip(*results):
+        assert torch.equal(a, b) and a.isfinite().all()
+
+
 def run_muon(sl, theta, momentum, grad, **kw):
     t, m = theta.cuda(), momentum.cuda()
     sl.muon_step(t, m, grad.cuda(), **kw)
