@@ -152,7 +152,7 @@ def sl_orthogonalize(x: torch.Tensor, out: torch.Tensor, coefficients=SL_NEWTON_
     """out = the Newton-Schulz orthogonalisation of x ([rows, cols] or [count,
     rows, cols], float32, bfloat16 or float16, adjacent columns; rows and
     matrices may be strided).  products: 'f16' (within about 1e-3 of the exact
-    result) or 'split' (about 3e-6, three times the products); by default
+    result) or 'split' (as fp32 arithmetic, three times the products); by default
     'split' for a float32 out and 'f16' for a 16-bit one.  workspace: a buffer
     of orthogonalize_workspace() bytes to use again; by default one from torch's
     allocator."""

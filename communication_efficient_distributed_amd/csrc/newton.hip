@@ -660,8 +660,16 @@ Plan plan_of(int64_t rows, int64_t cols, int64_t count, bool split, bool update)
     p.xt1 = take(p.m * p.n);
     p.a = take(p.m * p.m);
     p.b = take(p.m * p.m);
-    // The products of square matrices have to be large enough to run at full rate.
-    p.by_gram = update && split && p.tile == 4 && 2 * n >= 3 * m;
+    // That way takes about 9 square products more than the other, and 3 Gram
+    // matrices and 3 products of the long side less.  Even at n = 2 m for 128 x
+    // 128 tiles (3 x 1000 x 2000 591 us both, 3 x 1000 x 2731 812 -> 700, 1024 x
+    // 8192 673 -> 514) and for 64 x 64 tiles if the square products fill a good
+    // part of the chip (20 x 300 x 700 281 -> 250); if not, their latency wants
+    // more (500 x 2000 186 -> 204, 300 x 4000 173 -> 166 us).  With 256 x 256
+    // tiles its result is less exact, about 1e-5 for singular values that span
+    // decades, which a weight update does not see.
+    const bool fills = tiles(64) >= 64 || n >= 8 * m;
+    p.by_gram = split && (p.tile == 4 ? update && 2 * n >= 3 * m : n >= 2 * m && (p.tile == 2 || fills));
     if (p.by_gram)
         for (int64_t& c : p.c) c = take(p.m * p.m);
     p.lo = at / 2;
@@ -787,14 +795,20 @@ hipError_t run_products(const UpdateArgs& u, const Plan& p, char* ws, hipStream_
     return hipGetLastError();
 }
 
-// Steps between two Gram matrices of X, and how much Q may grow over them.
-constexpr int kTogether = 3;
+// Steps between two Gram matrices of X, and how much Q may grow over them.  A
+// rounding of R is stretched by up to 11.9 with each step of the usual
+// coefficients, against which a large m helps (the errors of R's entries are
+// independent): with three steps 64 x 20000 is 6.3e-6 off where one singular
+// value outweighs the others ten times, 130 x 8000 5.3e-6 and 1024 x 8192
+// 2.4e-6 (3.6e-6 in plain fp32); with two 2.1e-6 and 1.4e-6, but 130 x 8000 by
+// 16 takes 480 us and not 376.
+int together_of(const Plan& p) { return p.m >= 512 ? 3 : 2; }
 constexpr float kMaxGrowth = 256.0f;
 
-// |Q|'s bound over the steps from `from` on, up to kTogether of them.
-float growth_of(const UpdateArgs& u, int from) {
+// |Q|'s bound over the steps [from, to).
+float growth_of(const UpdateArgs& u, int from, int to) {
     float most = 1, product = 1;
-    for (int s = from; s < u.n_steps && s < from + kTogether; ++s) {
+    for (int s = from; s < u.n_steps && s < to; ++s) {
         product *= u.factors[s];
         if (product > most) most = product;
         if (u.factors[s] > most) most = u.factors[s];
@@ -802,10 +816,12 @@ float growth_of(const UpdateArgs& u, int from) {
     return most;
 }
 
+template <int T>
 hipError_t run_by_gram(const UpdateArgs& u, const Plan& p, char* ws, hipStream_t stream) {
     constexpr float kScaleR = 2048.0f;  // |R| and |P R| are at most 3.8^2
+    constexpr int kTerms = T < 4 ? kPaired : kInTurn;
     const bool tall = u.rows > u.cols;
-    const int tm = (int)(p.m / 256), tn = (int)(p.n / 256);
+    const int tm = (int)(p.m / (64 * T)), tn = (int)(p.n / (64 * T));
     auto at = [&](int64_t o) { return reinterpret_cast<_Float16*>(ws + o); };
     ProductArgs g = {};
     g.lo = p.lo;
@@ -821,14 +837,15 @@ hipError_t run_by_gram(const UpdateArgs& u, const Plan& p, char* ws, hipStream_t
         g.old = old < 0 ? nullptr : at(old);
         g.c = g.ct = at(to);
         g.alpha = alpha, g.beta = beta, g.gamma = gamma;
-        run_symmetric<4, kInTurn, kSym>(g, p.whole, p.poly_slices, u.count, stream);
+        run_symmetric<T, kTerms, kSym>(g, p.whole, p.poly_slices, u.count, stream);
     };
     const int64_t r = p.a, t = p.b;
     int64_t xt = p.xt0, xt_next = p.xt1;
-    for (int from = 0; from < u.n_steps; from += kTogether) {
-        const int to = from + kTogether < u.n_steps ? from + kTogether : u.n_steps;
+    const int together = together_of(p);
+    for (int from = 0; from < u.n_steps; from += together) {
+        const int to = from + together < u.n_steps ? from + together : u.n_steps;
         float scale = 16384.0f;  // of P and Q
-        for (float f = 1; f < growth_of(u, from); f *= 2) scale *= 0.5f;
+        for (float f = 1; f < growth_of(u, from, to); f *= 2) scale *= 0.5f;
         g.tiles_i = g.tiles_j = tm;
         g.p = g.q = at(p.x);
         g.ldp = g.ldq = p.n;
@@ -837,7 +854,7 @@ hipError_t run_by_gram(const UpdateArgs& u, const Plan& p, char* ws, hipStream_t
         g.old = nullptr;
         g.c = g.ct = at(r);
         g.alpha = kScaleR / (kScaleX * kScaleX), g.beta = g.gamma = 0;
-        run_symmetric<4, kInTurn, kSym>(g, p.whole, p.gram_slices, u.count, stream);
+        run_symmetric<T, kInTurn, kSym>(g, p.whole, p.gram_slices, u.count, stream);
         int64_t poly = p.c[0], q = p.c[1], q_next = p.c[2];
         for (int s = from; s < to; ++s) {
             const Quintic& k = u.steps[s];
@@ -866,7 +883,7 @@ hipError_t run_by_gram(const UpdateArgs& u, const Plan& p, char* ws, hipStream_t
             g.c = at(p.x), g.ldc = p.n;
             g.ct = at(xt_next), g.ldct = p.m;
             g.alpha = 1 / scale;
-            product_kernel<4, 4, kInTurn, kFull><<<full, 256, 0, stream>>>(g);
+            product_kernel<T, T, kTerms, kFull><<<full, 256, 0, stream>>>(g);
             const int64_t was = xt;
             xt = xt_next;
             xt_next = was;
@@ -877,7 +894,7 @@ hipError_t run_by_gram(const UpdateArgs& u, const Plan& p, char* ws, hipStream_t
             g.q = at(tall ? xt : q);
             g.tiles_i = tall ? tm : tn;
             g.tiles_j = tall ? tn : tm;
-            product_kernel<4, 4, kInTurn, kEnd><<<full, 256, 0, stream>>>(g);
+            product_kernel<T, T, kTerms, kEnd><<<full, 256, 0, stream>>>(g);
         }
     }
     return hipGetLastError();
@@ -906,8 +923,12 @@ hipError_t run(const UpdateArgs& u, const Plan& p, char* ws, hipStream_t stream)
         s, u.rows, u.cols, sums, p.sum_blocks, u.eps, direct, pc, turned, pr, p.lo, p.matrix_bytes);
     if (p.by_gram) {
         float most = 0;
-        for (int from = 0; from < u.n_steps; from += kTogether) most = fmaxf(most, growth_of(u, from));
-        if (most <= kMaxGrowth) return run_by_gram(u, p, ws, stream);
+        const int together = together_of(p);
+        for (int from = 0; from < u.n_steps; from += together) most = fmaxf(most, growth_of(u, from, from + together));
+        if (most <= kMaxGrowth)
+            return p.tile == 4   ? run_by_gram<4>(u, p, ws, stream)
+                   : p.tile == 2 ? run_by_gram<2>(u, p, ws, stream)
+                                 : run_by_gram<1>(u, p, ws, stream);
     }
     if (p.tile == 4) return run_products<4, SPLIT>(u, p, ws, stream);
     if (p.tile == 2) return run_products<2, SPLIT>(u, p, ws, stream);

@@ -38,9 +38,12 @@ typedef enum {
                              within about 1e-3 of the exact one (2-norm of the
                              difference over 2-norm), finer than bf16 holds */
     SL_PRODUCTS_SPLIT = 1 /* each operand the sum of two fp16 values (22 bits), three
-                             products: within about 3e-6, at three times the work
-                             (sl_muon_step on matrices of some thousand rows and
-                             columns that are not square: about 1e-5) */
+                             products: within about what fp32 arithmetic leaves
+                             (1e-6 to 3e-6, and more where singular values span
+                             decades: 2e-5 if one outweighs the others a hundred
+                             times), at three times the work.  sl_muon_step on
+                             matrices of some thousand rows and columns that are
+                             not square: about 1e-5 */
 } sl_products;
 
 #define SL_MAX_STEPS 16
