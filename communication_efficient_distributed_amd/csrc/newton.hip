@@ -23,6 +23,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "newton.h"
 
 namespace sl {
@@ -609,8 +611,9 @@ struct Plan {
     int64_t sums, part;    // byte offsets of the partial sums of squares and of sliced products
     int64_t total;
     int sum_blocks;
-    int64_t whole;         // tiles of a symmetric product that are not sliced
-    int gram_slices, poly_slices;
+    int square;            // the tile of products of square matrices
+    int64_t gram_whole, square_whole;  // tiles of a symmetric product that are not sliced
+    int gram_slices, square_slices;    // slices of the others
 };
 
 // Four consecutive elements of a row, from a multiple of four on, lie in one aligned word.
@@ -686,13 +689,19 @@ Plan plan_of(int64_t rows, int64_t cols, int64_t count, bool split, bool update)
     const int64_t pieces = (rows * cols + 2047) / 2048, most = round_up(kSumBlocks / count + 1, 64);
     p.sum_blocks = (int)(pieces < most ? pieces : most);
     p.part = p.sums + round_up(count * p.sum_blocks * 8, 256);
-    const int64_t sym = tiles(64 * p.tile), per_step = split ? p.tile < 4 ? 2 : 3 : 1;
-    p.whole = whole_of(sym, p.tile);
-    p.gram_slices = slices_of(sym - p.whole, (split ? 3 : 1) * p.n / 64, p.tile);
-    p.poly_slices = slices_of(sym - p.whole, per_step * p.m / 64, p.tile);
-    const int64_t slices = p.gram_slices > p.poly_slices ? p.gram_slices : p.poly_slices;
+    // Square products by themselves fill less of the chip: smaller tiles up to
+    // some size (600 x 9000 357 -> 312 us, 1024 x 8192 505 -> 490, 8 x 600 x
+    // 3000 671 -> 660; 2 x 1000 x 5000 635 -> 645, 2048 x 8192 1355 -> 1539).
+    p.square = p.by_gram && p.tile == 2 && (double)count * m * m * m <= 1.8e9 ? 1 : p.tile;
+    const int64_t sym = tiles(64 * p.tile), square_sym = tiles(64 * p.square), per_step = split ? p.tile < 4 ? 2 : 3 : 1;
+    p.gram_whole = whole_of(sym, p.tile);
+    p.square_whole = whole_of(square_sym, p.square);
+    p.gram_slices = slices_of(sym - p.gram_whole, (split ? 3 : 1) * p.n / 64, p.tile);
+    p.square_slices = slices_of(square_sym - p.square_whole, per_step * p.m / 64, p.square);
     // The sums of squares lie behind what either way needs.
-    p.total = p.part + (slices > 1 ? (sym - p.whole) * slices * p.tile * p.tile * 4 * 256 * 16 : 0);
+    auto parts = [](int64_t n, int64_t slices, int64_t tile) { return slices > 1 ? n * slices * tile * tile * 4 * 256 * 16 : 0; };
+    p.total = p.part + std::max(parts(sym - p.gram_whole, p.gram_slices, p.tile),
+                                parts(square_sym - p.square_whole, p.square_slices, p.square));
     return p;
 }
 
@@ -753,7 +762,7 @@ hipError_t run_products(const UpdateArgs& u, const Plan& p, char* ws, hipStream_
         g.diag_in = nullptr;
         g.diag_out = reinterpret_cast<float*>(ws + p.da);
         g.alpha = kScaleA / (kScaleX * kScaleX), g.beta = g.gamma = 0;
-        run_symmetric<T, kGramTerms, kGramKind>(g, p.whole, p.gram_slices, u.count, stream);
+        run_symmetric<T, kGramTerms, kGramKind>(g, p.gram_whole, p.gram_slices, u.count, stream);
         g.p = g.q = g.old = at(p.a);
         g.ldp = g.ldq = g.ldold = p.m;
         g.k_steps = (int)(p.m / 64);
@@ -764,7 +773,7 @@ hipError_t run_products(const UpdateArgs& u, const Plan& p, char* ws, hipStream_
         float p_scale = 16384.0f;
         for (float f = 1; f < u.factors[s]; f *= 2) p_scale *= 0.5f;
         g.alpha = g.k.c * p_scale / (kScaleA * kScaleA), g.beta = g.k.b * p_scale / kScaleA, g.gamma = g.k.a * p_scale;
-        run_symmetric<T, kTerms, kPolyKind>(g, p.whole, p.poly_slices, u.count, stream);
+        run_symmetric<T, kTerms, kPolyKind>(g, p.square_whole, p.square_slices, u.count, stream);
         g.diag_in = reinterpret_cast<const float*>(ws + p.db);
         g.diag_out = nullptr;
         g.alpha = 1 / p_scale;
@@ -795,6 +804,12 @@ hipError_t run_products(const UpdateArgs& u, const Plan& p, char* ws, hipStream_
     return hipGetLastError();
 }
 
+// The way by the Gram matrix.  Every step multiplies X by a polynomial of A,
+// so a few steps together need one Gram matrix R = X X^T and one product of
+// the long side, with square products in between:
+//     P = a I + b R + c R R,  Q <- Q P,  R <- P R P       (Q = P at first)
+// and X <- Q X in the end.  All of P, Q, R are symmetric and commute.
+
 // Steps between two Gram matrices of X, and how much Q may grow over them.  A
 // rounding of R is stretched by up to 11.9 with each step of the usual
 // coefficients, against which a large m helps (the errors of R's entries are
@@ -816,10 +831,10 @@ float growth_of(const UpdateArgs& u, int from, int to) {
     return most;
 }
 
-template <int T>
+template <int T, int SQUARE>
 hipError_t run_by_gram(const UpdateArgs& u, const Plan& p, char* ws, hipStream_t stream) {
     constexpr float kScaleR = 2048.0f;  // |R| and |P R| are at most 3.8^2
-    constexpr int kTerms = T < 4 ? kPaired : kInTurn;
+    constexpr int kTerms = T < 4 ? kPaired : kInTurn, kSquareTerms = SQUARE < 4 ? kPaired : kInTurn;
     const bool tall = u.rows > u.cols;
     const int tm = (int)(p.m / (64 * T)), tn = (int)(p.n / (64 * T));
     auto at = [&](int64_t o) { return reinterpret_cast<_Float16*>(ws + o); };
@@ -830,14 +845,14 @@ hipError_t run_by_gram(const UpdateArgs& u, const Plan& p, char* ws, hipStream_t
     const unsigned full = (unsigned)(u.count * tm * tn);
     // to = alpha a b + beta old + gamma I, all m x m.
     auto square = [&](int64_t to, int64_t a, int64_t b, float alpha, int64_t old, float beta, float gamma) {
-        g.tiles_i = g.tiles_j = tm;
+        g.tiles_i = g.tiles_j = tm * T / SQUARE;
         g.p = at(a), g.q = at(b);
         g.ldp = g.ldq = g.ldold = g.ldc = g.ldct = p.m;
         g.k_steps = (int)(p.m / 64);
         g.old = old < 0 ? nullptr : at(old);
         g.c = g.ct = at(to);
         g.alpha = alpha, g.beta = beta, g.gamma = gamma;
-        run_symmetric<T, kTerms, kSym>(g, p.whole, p.poly_slices, u.count, stream);
+        run_symmetric<SQUARE, kSquareTerms, kSym>(g, p.square_whole, p.square_slices, u.count, stream);
     };
     const int64_t r = p.a, t = p.b;
     int64_t xt = p.xt0, xt_next = p.xt1;
@@ -854,7 +869,7 @@ hipError_t run_by_gram(const UpdateArgs& u, const Plan& p, char* ws, hipStream_t
         g.old = nullptr;
         g.c = g.ct = at(r);
         g.alpha = kScaleR / (kScaleX * kScaleX), g.beta = g.gamma = 0;
-        run_symmetric<T, kInTurn, kSym>(g, p.whole, p.gram_slices, u.count, stream);
+        run_symmetric<T, kInTurn, kSym>(g, p.gram_whole, p.gram_slices, u.count, stream);
         int64_t poly = p.c[0], q = p.c[1], q_next = p.c[2];
         for (int s = from; s < to; ++s) {
             const Quintic& k = u.steps[s];
@@ -926,9 +941,10 @@ hipError_t run(const UpdateArgs& u, const Plan& p, char* ws, hipStream_t stream)
         const int together = together_of(p);
         for (int from = 0; from < u.n_steps; from += together) most = fmaxf(most, growth_of(u, from, from + together));
         if (most <= kMaxGrowth)
-            return p.tile == 4   ? run_by_gram<4>(u, p, ws, stream)
-                   : p.tile == 2 ? run_by_gram<2>(u, p, ws, stream)
-                                 : run_by_gram<1>(u, p, ws, stream);
+            return p.tile == 4     ? run_by_gram<4, 4>(u, p, ws, stream)
+                   : p.square == 2 ? run_by_gram<2, 2>(u, p, ws, stream)
+                   : p.tile == 2   ? run_by_gram<2, 1>(u, p, ws, stream)
+                                   : run_by_gram<1, 1>(u, p, ws, stream);
     }
     if (p.tile == 4) return run_products<4, SPLIT>(u, p, ws, stream);
     if (p.tile == 2) return run_products<2, SPLIT>(u, p, ws, stream);
