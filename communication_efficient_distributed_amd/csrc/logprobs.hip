@@ -18,6 +18,10 @@
 // Enough rows (or a small vocabulary) give every row a block of its own, which
 // scans and finishes it; few rows are split over the vocabulary and joined by a
 // second kernel.
+//
+// Bound by memory where there are many rows: 1024 x 262208 bf16 88 us, 6.1
+// TB/s; 4096 x 262208 with five alternatives 355 us, 6.05 TB/s.  One row is bound by
+// latency: 20 us with 20 alternatives, 6 the scan and 12 the finish.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -157,8 +161,8 @@ __device__ __forceinline__ int lead_of(const typename Element<TYPE>::type* row) 
 
 // Positions [at, at + kVector) of a row: one aligned load inside the row,
 // single tokens (and -inf beyond) at its ends.  ONCE: loads that pass the
-// caches by, for the scan: 8192 x 131072 bytes of a row each read at 6.8 TB/s
-// so and at 6.0 TB/s without.
+// caches by, for the scan: 2048 rows of 131072 fp32 were read at 6.8 TB/s so
+// and at 6.0 TB/s without.
 typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
 
 template <int TYPE, bool ONCE>

@@ -19,6 +19,13 @@
 // range: X is stored times 2^13, A times 2^12, B times 2^11, for which the
 // host refuses coefficients whose iterates could pass 3.8 (|X_ij| <= |X|_2,
 // |A_ij| <= |X|_2^2) or 30 for |B|_2.
+//
+// Large matrices are bound by the matrix cores at the clock that their power
+// leaves: 8192 x 8192 bf16 9.7 ms for 11 TFLOP (1.13 PFLOP/s; a library fp16
+// product of that size runs at 1.34).  Small ones are bound by the latency of
+// a chain of 17 to 36 launches.  Split products of matrices twice as long as
+// wide, or more, go by the Gram matrix alone (run_by_gram), fp16 products of
+// up to 128 rows or columns by newton_narrow.hip.
 #include <hip/hip_fp16.h>
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -41,7 +48,8 @@ constexpr int kSumBlocks = 1024;  // of all matrices' partial sums of squares, a
 // in fp64 (no overflow or underflow for any finite fp32 values); momentum is
 // updated on the way.  Blocks take pieces of 2048 columns of a row in turn, a
 // thread eight columns of each: in one go where the rows' alignment allows it
-// (VECTOR), else 256 apart.
+// (VECTOR), else 256 apart.  Bound by memory: 8192 x 28672 fp32 with momentum
+// (2.8 GB read and written) 0.60 ms, 4.7 TB/s.
 template <bool VECTOR>
 __global__ __launch_bounds__(256) void sum_squares_kernel(Source s, int64_t rows, int64_t cols, double* partial) {
     __shared__ double lds[4];
@@ -91,7 +99,9 @@ __global__ __launch_bounds__(256) void sum_squares_kernel(Source s, int64_t rows
 
 // X = u * 2^13 / (|u| + eps) as fp16 (hi, and lo if split) in both
 // orientations, zero beyond the matrix: direct[r][c] (ld_direct) and
-// turned[c][r] (ld_turned), 64 x 64 elements per block.
+// turned[c][r] (ld_turned), 64 x 64 elements per block.  Bound by memory, by
+// its writes of two bytes per lane: 8192 x 28672 with momentum, split (3.8 GB)
+// 0.70 ms, 5.4 TB/s; 8192 x 8192 bf16 (0.4 GB) 0.15 ms.
 template <bool SPLIT>
 __global__ __launch_bounds__(256) void start_kernel(Source s, int64_t rows, int64_t cols, const double* partial,
                                                     int n_partial, float eps, _Float16* direct, int64_t ld_direct,
@@ -395,10 +405,16 @@ struct Constant {
 // less LDS traffic, but half lines from memory.  Measured on whole calls: one
 // 1024 x 1024 409 against 345 us, three 1000 x 2731 867 against 830; but the
 // Gram matrix of 1024 x 8192 35 against 45 us, and 256 x 256 tiles (8192 x
-// 28672) 55.5 against 57.5 ms.  So: pairs for small tiles along the short side.  (Small
-// tiles gained nothing from three or four stages, and lost the blocks per
-// compute unit that their LDS takes: 8 x 1024 x 1024, 444 us in all with two
-// stages, 460 with three, 512 with four.)
+// 28672) 55.5 against 57.5 ms.  So: pairs for small tiles along the short
+// side.  (Small tiles gained nothing from three or four stages, and lost the
+// blocks per compute unit that their LDS takes: 8 x 1024 x 1024, 444 us in all
+// with two stages, 460 with three, 512 with four.)
+//
+// 256 x 256 tiles are bound by the matrix cores: 8192 x 8192 x 8192 plain 0.92
+// ms, 1.19 PFLOP/s with the cores busy 63% of the time at a clock that their
+// power holds down; split 8192 x 28672 x 8192 8.8 ms, 1.31 PFLOP/s, 70%.
+// Smaller tiles are bound by the latency of loads and the finish, all blocks
+// running at once: split 8192 x 1024 x 1024 63 us, 0.82 PFLOP/s, 37%.
 template <int TI, int TJ, int TERMS, int KIND>
 __global__ __launch_bounds__(256, 1) void product_kernel(ProductArgs g) {
     constexpr bool SPLIT = TERMS != kPlain, PAIRED = TERMS == kPaired;

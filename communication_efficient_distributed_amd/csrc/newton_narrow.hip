@@ -13,6 +13,11 @@
 // their linear terms from fp32 registers: an error in R's small eigenvalues grows
 // with them, which 11 bits would not survive.  X is fp16 as in the other way;
 // Q, whose entries grow up to `growth`, multiplies it as two terms.
+//
+// Bound by latency: eight 8192 x 128 bf16 take 85 us, of which the steps on
+// one compute unit each are 39 (VALU and LDS, writing pairs), the last product
+// 23, the Gram matrices 15 with their join 6, the norms 6; the 34 MB in and
+// out alone would take 5.  One 128 x 192 takes 63 us.
 #include "newton.h"
 
 namespace sl {
