@@ -627,9 +627,11 @@ struct Plan {
     int64_t sums, part;    // byte offsets of the partial sums of squares and of sliced products
     int64_t total;
     int sum_blocks;
-    int square;            // the tile of products of square matrices
-    int64_t gram_whole, square_whole;  // tiles of a symmetric product that are not sliced
-    int gram_slices, square_slices;    // slices of the others
+    int square;            // the tile of square products in the Gram matrix's way
+    // Of Gram matrices, of polynomials step by step and of square products:
+    // tiles that are not sliced, and slices of the others.
+    int64_t gram_whole, poly_whole, square_whole;
+    int gram_slices, poly_slices, square_slices;
 };
 
 // Four consecutive elements of a row, from a multiple of four on, lie in one aligned word.
@@ -714,14 +716,16 @@ Plan plan_of(int64_t rows, int64_t cols, int64_t count, bool split, bool update)
     // 3000 671 -> 660; 2 x 1000 x 5000 635 -> 645, 2048 x 8192 1355 -> 1539).
     p.square = p.by_gram && p.tile == 2 && (double)count * m * m * m <= 1.8e9 ? 1 : p.tile;
     const int64_t sym = tiles(64 * p.tile), square_sym = tiles(64 * p.square), per_step = split ? p.tile < 4 ? 2 : 3 : 1;
-    p.gram_whole = whole_of(sym, p.tile);
+    p.gram_whole = p.poly_whole = whole_of(sym, p.tile);
     p.square_whole = whole_of(square_sym, p.square);
     p.gram_slices = slices_of(sym - p.gram_whole, (split ? 3 : 1) * p.n / 64, p.tile);
+    p.poly_slices = slices_of(sym - p.poly_whole, per_step * p.m / 64, p.tile);
     p.square_slices = slices_of(square_sym - p.square_whole, per_step * p.m / 64, p.square);
     // The sums of squares lie behind what either way needs.
     auto parts = [](int64_t n, int64_t slices, int64_t tile) { return slices > 1 ? n * slices * tile * tile * 4 * 256 * 16 : 0; };
-    p.total = p.part + std::max(parts(sym - p.gram_whole, p.gram_slices, p.tile),
-                                parts(square_sym - p.square_whole, p.square_slices, p.square));
+    p.total = p.part + std::max({parts(sym - p.gram_whole, p.gram_slices, p.tile),
+                                 parts(sym - p.poly_whole, p.poly_slices, p.tile),
+                                 parts(square_sym - p.square_whole, p.square_slices, p.square)});
     return p;
 }
 
@@ -793,7 +797,7 @@ hipError_t run_products(const UpdateArgs& u, const Plan& p, char* ws, hipStream_
         float p_scale = 16384.0f;
         for (float f = 1; f < u.factors[s]; f *= 2) p_scale *= 0.5f;
         g.alpha = g.k.c * p_scale / (kScaleA * kScaleA), g.beta = g.k.b * p_scale / kScaleA, g.gamma = g.k.a * p_scale;
-        run_symmetric<T, kTerms, kPolyKind>(g, p.square_whole, p.square_slices, u.count, stream);
+        run_symmetric<T, kTerms, kPolyKind>(g, p.poly_whole, p.poly_slices, u.count, stream);
         g.diag_in = reinterpret_cast<const float*>(ws + p.db);
         g.diag_out = nullptr;
         g.alpha = 1 / p_scale;

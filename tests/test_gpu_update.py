@@ -309,6 +309,26 @@ def test_split_products_of_long_matrices_by_their_gram_matrix(count, rows, cols)
     assert not zero.any()
 
 
+@pytest.mark.parametrize("count,rows,cols", [(1, 600, 9000), (1, 1300, 2800), (1, 8192, 1024), (1, 520, 4300)])
+def test_steep_steps_of_long_matrices_stay_in_their_workspace(count, rows, cols):
+    """Sizes that go by the Gram matrix, with coefficients that do not: on a workspace of exactly the stated size."""
+    sl = require_gpu()
+    note(f"steep steps {count}x{rows}x{cols}")
+    steps = ((3.7, -5.3, 2.2), (8.0, -14.0, 6.0), (9.0, -8.0, 1.2))
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    x = torch.randn((count, rows, cols), generator=g, device="cuda")
+    need = sl.orthogonalize_workspace(rows, cols, count, "split")
+    whole = torch.full((need + (64 << 20),), 170, dtype=torch.uint8, device="cuda")
+    for coefficients in (steps, STEPS):
+        out = torch.empty_like(x)
+        sl.sl_orthogonalize(x, out, coefficients=coefficients, workspace=whole[:need])
+        assert (whole[need:] == 170).all()
+        want = newton_schulz(x[0], coefficients)
+        # the steep steps' bound, as the other way has it; that of the Gram matrix's for the usual ones
+        tol = newton_schulz_tolerance(x[0], want, True, coefficients) if coefficients is steps else 2 * 1.1e-5
+        assert relative(out[0], want) <= tol
+
+
 def test_muon_step_is_the_composition():
     """theta's move is what sl_orthogonalize gives for the same u: bitwise with keep 1 and move 1 from zero weights."""
     sl = require_gpu()
