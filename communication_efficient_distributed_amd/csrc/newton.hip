@@ -690,11 +690,13 @@ Plan plan_of(int64_t rows, int64_t cols, int64_t count, bool split, bool update)
     // 128 tiles (3 x 1000 x 2000 591 us both, 3 x 1000 x 2731 812 -> 700, 1024 x
     // 8192 673 -> 514) and for 64 x 64 tiles if the square products fill a good
     // part of the chip (20 x 300 x 700 281 -> 250); if not, their latency wants
-    // more (500 x 2000 186 -> 204, 300 x 4000 173 -> 166 us).  With 256 x 256
+    // more (500 x 2000 186 -> 204, 300 x 4000 173 -> 166 us).  Below 256 rows the
+    // result is less exact than fp32 arithmetic's, which a small m leaves at
+    // 1e-6 (1.9e-6 against 1.1e-6), though faster.  With 256 x 256
     // tiles its result is less exact, about 1e-5 for singular values that span
     // decades, which a weight update does not see.
     const bool fills = tiles(64) >= 64 || n >= 8 * m;
-    p.by_gram = split && (p.tile == 4 ? update && 2 * n >= 3 * m : n >= 2 * m && (p.tile == 2 || fills));
+    p.by_gram = split && (p.tile == 4 ? update && 2 * n >= 3 * m : m >= 256 && n >= 2 * m && (p.tile == 2 || fills));
     if (p.by_gram)
         for (int64_t& c : p.c) c = take(p.m * p.m);
     p.lo = at / 2;
@@ -837,10 +839,9 @@ hipError_t run_products(const UpdateArgs& u, const Plan& p, char* ws, hipStream_
 // Steps between two Gram matrices of X, and how much Q may grow over them.  A
 // rounding of R is stretched by up to 11.9 with each step of the usual
 // coefficients, against which a large m helps (the errors of R's entries are
-// independent): with three steps 64 x 20000 is 6.3e-6 off where one singular
-// value outweighs the others ten times, 130 x 8000 5.3e-6 and 1024 x 8192
-// 2.4e-6 (3.6e-6 in plain fp32); with two 2.1e-6 and 1.4e-6, but 130 x 8000 by
-// 16 takes 480 us and not 376.
+// independent): where one singular value outweighs the others ten times, 300 x
+// 4000 is 3.0e-6 off with three steps and 1.5e-6 with two (plain fp32 2.2e-6;
+// 161 and 166 us), 1024 x 8192 2.4e-6 with three (plain fp32 3.6e-6).
 int together_of(const Plan& p) { return p.m >= 512 ? 3 : 2; }
 constexpr float kMaxGrowth = 256.0f;
 
