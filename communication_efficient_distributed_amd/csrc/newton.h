@@ -77,8 +77,8 @@ __device__ __forceinline__ void split_half(float v, _Float16* hi, _Float16* lo) 
     *lo = (_Float16)(v - (float)*hi);
 }
 
-// The update of matrices whose shorter side is at most kNarrow, by way of the
-// Gram matrix alone; false products only.  partial: n_partial partial sums of
+// The update of long matrices whose shorter side is at most kNarrow, by way of
+// the Gram matrix alone; false products only.  partial: n_partial partial sums of
 // squares for each matrix.
 constexpr int64_t kNarrow = 128;
 bool is_narrow(const UpdateArgs& u);

@@ -25,7 +25,7 @@
 // product of that size runs at 1.34).  Small ones are bound by the latency of
 // a chain of 17 to 36 launches.  Split products of matrices twice as long as
 // wide, or more, go by the Gram matrix alone (run_by_gram), fp16 products of
-// up to 128 rows or columns by newton_narrow.hip.
+// long matrices of up to 128 rows or columns by newton_narrow.hip.
 #include <hip/hip_fp16.h>
 #include <hip/hip_runtime.h>
 #include <stdint.h>

@@ -1,5 +1,6 @@
 // newton_narrow.hip -- the matrix update for matrices whose shorter side m is
-// at most 128 (attention heads, small projections), fp16 products.
+// at most 128 and whose longer one is eight times that or more (attention
+// heads), fp16 products.
 //
 // Every step multiplies X by a polynomial of its Gram matrix, so all of them
 // can be worked out on m x m matrices: with R = X X^T, for each (a, b, c)
@@ -17,7 +18,7 @@
 // Bound by latency: eight 8192 x 128 bf16 take 85 us, of which the steps on
 // one compute unit each are 39 (VALU and LDS, writing pairs), the last product
 // 23, the Gram matrices 15 with their join 6, the norms 6; the 34 MB in and
-// out alone would take 5.  One 128 x 192 takes 63 us.
+// out alone would take 5.
 #include "newton.h"
 
 namespace sl {
@@ -454,9 +455,13 @@ void run_steps(int64_t count, const float4* gram, int slices, const Steps& steps
 
 }  // namespace
 
-// Growth beyond kMaxGrowth would push Q's 22 bits into the result.
+// Growth beyond kMaxGrowth would push Q's 22 bits into the result.  R's
+// roundings are stretched where singular values are small, as they are unless
+// the matrix is long: this way is up to 8e-3 off at 64 x 96 and 2e-3 at 128 x
+// 192 where the other stays within 1.2e-3; at 128 x 512 4e-4 against 8e-4.
 bool is_narrow(const UpdateArgs& u) {
-    return !u.split && (u.rows < u.cols ? u.rows : u.cols) <= kNarrow && u.growth <= kMaxGrowth;
+    const int64_t m = u.rows < u.cols ? u.rows : u.cols, n = u.rows < u.cols ? u.cols : u.rows;
+    return !u.split && m <= kNarrow && n >= 8 * m && n >= 512 && u.growth <= kMaxGrowth;
 }
 
 size_t narrow_workspace_bytes(int64_t rows, int64_t cols, int64_t count) { return (size_t)layout_of(rows, cols, count).total; }

@@ -309,6 +309,15 @@ def test_split_products_of_long_matrices_by_their_gram_matrix(count, rows, cols)
     assert not zero.any()
 
 
+@pytest.mark.parametrize("rows,cols", [(96, 64), (80, 64), (140, 128), (50, 40), (24, 16), (64, 96), (256, 64), (520, 64)])
+def test_plain_products_of_tall_matrices_with_uneven_rows(rows, cols):
+    """Small singular values, which roundings of the Gram matrix would drown."""
+    sl = require_gpu()
+    note(f"plain products, uneven rows {rows}x{cols}")
+    x = update_like((12, rows, cols), 7 * rows + cols)
+    check(sl.orthogonalize(x.cuda(), products="f16"), x, "f16")
+
+
 @pytest.mark.parametrize("count,rows,cols", [(1, 600, 9000), (1, 1300, 2800), (1, 8192, 1024), (1, 520, 4300)])
 def test_steep_steps_of_long_matrices_stay_in_their_workspace(count, rows, cols):
     """Sizes that go by the Gram matrix, with coefficients that do not: on a workspace of exactly the stated size."""
